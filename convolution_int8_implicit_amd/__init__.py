@@ -10,13 +10,15 @@ Entry points mirror include/ifx.h:
     conv_validate, conv_out_dims, act_bytes, wpack_bytes,
     pack_act, unpack_act, pack_weights, conv_fused,
     block_workspace_bytes, block_forward, net_workspace_bytes, net_forward,
-    fold_bn, status_string, last_hip_error, version
+    fold_bn, status_string, last_hip_error, version,
+    mx4_quantize, mx4_dequantize, mx4_matmul (microscaled 4-bit floating point),
+    group_norm, group_norm_mx4, group_norm_backward (channels last)
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -28,9 +30,12 @@ __all__ = [
     "block_workspace_bytes", "block_forward", "block_forward_noalloc",
     "BLOCK_SCRATCH_BYTES", "net_workspace_bytes",
     "net_forward", "NetGraph", "fold_bn", "BnFold", "status_string", "last_hip_error", "version", "LIB_PATH",
+    "ACT_NONE", "ACT_RELU", "ACT_SILU", "Mx4", "mx4_empty", "mx4_quantize", "mx4_dequantize", "mx4_matmul",
+    "group_norm", "group_norm_mx4", "group_norm_backward",
 ]
 
 RELU, RESIDUAL, MAXPOOL, OUT_I32, INPUT_NHWC, OUT_EVEN, OUT_PHASE, IN_PHASE = 1, 2, 4, 8, 16, 32, 64, 128
+ACT_NONE, ACT_RELU, ACT_SILU = 0, 1, 2
 STATUS = {0: "IFX_OK", 1: "IFX_E_NULL", 2: "IFX_E_SHAPE", 3: "IFX_E_UNSUPPORTED", 4: "IFX_E_ALIGN",
           5: "IFX_E_WORKSPACE", 6: "IFX_E_HIP"}
 
@@ -71,6 +76,17 @@ class BnFold(ctypes.Structure):
                 ("eps", ctypes.c_float), ("w_per_channel", ctypes.c_int32), ("w_scale", ctypes.c_void_p),
                 ("conv_bias", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p),
                 ("mean", ctypes.c_void_p), ("var", ctypes.c_void_p)]
+
+
+class Mx4Desc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("ld_y", ctypes.c_int64), ("ld_res", ctypes.c_int64)]
+
+
+class GnDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("hw", ctypes.c_int32), ("c", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float), ("ld_x", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("ld_dy", ctypes.c_int64)]
 
 
 _LIB = None
@@ -118,6 +134,15 @@ def lib() -> ctypes.CDLL:
         "ifx_conv_proj_chain_kernel_name": ([D, D, D, ctypes.c_char_p, sz], i32),
         "ifx_conv_proj_chain_fused": ([D, vp, vp, vp, vp, vp, D, vp, vp, vp, vp, vp, vp, D, vp, vp, vp, vp, vp,
                                        vp], i32),
+        "ifx_mx4_code_bytes": ([i32, i32], sz),
+        "ifx_mx4_scale_bytes": ([i32, i32], sz),
+        "ifx_mx4_quantize": ([vp, i32, i64, i32, i32, vp, vp, vp], i32),
+        "ifx_mx4_dequantize": ([vp, vp, i32, i32, vp, i32, i64, vp], i32),
+        "ifx_mx4_matmul": ([ctypes.POINTER(Mx4Desc), vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        "ifx_group_norm_workspace_bytes": ([ctypes.POINTER(GnDesc), i32], sz),
+        "ifx_group_norm": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "ifx_group_norm_mx4": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "ifx_group_norm_backward": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
         "ifx_status_string": ([i32], ctypes.c_char_p),
         "ifx_probe_copy": ([vp, vp, sz, vp], i32),
         "ifx_probe_mfma_i8": ([vp, i32, i32, vp], i32),
@@ -427,6 +452,239 @@ def fold_bn(x_scale: float, y_scale: float, eps: float, w_scale: torch.Tensor, g
     outs = [torch.empty(n, dtype=torch.int32, device=gamma.device) for _ in range(4)]
     _check(lib().ifx_fold_bn(ctypes.byref(f), *[_ptr(o) for o in outs], _stream(stream)), "ifx_fold_bn")
     return tuple(outs)
+
+
+# ---------------------------------------------------------------------------
+# Microscaled 4-bit tensors and group norm
+# ---------------------------------------------------------------------------
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _type(dtype: torch.dtype) -> int:
+    if dtype not in _TYPES:
+        raise TypeError(f"float32, bfloat16 or float16 expected, not {dtype}")
+    return _TYPES[dtype]
+
+
+def _on_device(*ts) -> torch.device:
+    """The device of the tensors given: one GPU, the current one (the library launches there)."""
+    devices = {t.device for t in ts if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError(f"tensors of one GPU expected, not {sorted(map(str, devices))}")
+    device = devices.pop()
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _pitch(t: torch.Tensor):
+    """(rows, columns, elements from row to row) of a tensor whose last axis is contiguous and whose
+    other axes step as one: a contiguous tensor, or a slice of the last axis of one."""
+    if t.dim() == 0:
+        raise ValueError("a tensor of one or more axes expected")
+    k = t.shape[-1]
+    if t.numel() == 0:
+        return t.numel() // k if k else 0, k, k
+    rows, ld = 1, None
+    ok = k == 1 or t.stride(-1) == 1
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        ok = ok and stride == ld * rows
+        rows *= size
+    ld = k if ld is None else ld
+    if not ok or ld < k:
+        raise ValueError(f"rows of shape {tuple(t.shape)} and strides {t.stride()} do not lie at one pitch")
+    return rows, k, ld
+
+
+def _alloc(shape, dtype, device, stream) -> torch.Tensor:
+    """Uninitialised memory that belongs to the stream that will use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _param(t: Optional[torch.Tensor], n: int, name: str) -> None:
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{name}: contiguous float32 of shape ({n},) expected")
+
+
+class Mx4(NamedTuple):
+    """A microscaled 4-bit tensor of codes.shape[1] rows and k columns (layout: include/ifx.h):
+    codes uint8 [ceil(k / 128), rows, 64], scales uint8 [ceil(k / 128), rows, 4]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    k: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[1]
+
+
+def mx4_empty(rows: int, k: int, device="cuda", stream=None) -> Mx4:
+    k1 = (k + 127) // 128
+    return Mx4(_alloc((k1, rows, 64), torch.uint8, device, stream), _alloc((k1, rows, 4), torch.uint8, device, stream), k)
+
+
+def _mx4_check(q: Mx4, name: str) -> None:
+    k1 = (q.k + 127) // 128
+    for t, last in ((q.codes, 64), (q.scales, 4)):
+        if t.dtype != torch.uint8 or t.dim() != 3 or t.shape[0] != k1 or t.shape[2] != last or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous uint8 [{k1}, rows, {last}] expected for k = {q.k}")
+    if q.codes.shape[1] != q.scales.shape[1]:
+        raise ValueError(f"{name}: codes and scales of as many rows expected")
+
+
+def mx4_quantize(x: torch.Tensor, out: Optional[Mx4] = None, stream=None) -> Mx4:
+    """x [..., k] (float32, bfloat16 or float16) rounded to microscaled 4-bit codes, a row per leading
+    index (ifx_mx4_quantize)."""
+    device = _on_device(x, *(out[:2] if out is not None else ()))
+    rows, k, ld = _pitch(x)
+    if out is None:
+        out = mx4_empty(rows, k, device, stream)
+    _mx4_check(out, "out")
+    if (out.rows, out.k) != (rows, k):
+        raise ValueError(f"out of {out.rows} x {out.k}, x of {rows} x {k}")
+    _check(lib().ifx_mx4_quantize(_ptr(x), _type(x.dtype), ld, rows, k, _ptr(out.codes), _ptr(out.scales),
+                                  _stream(stream)), "ifx_mx4_quantize")
+    return out
+
+
+def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The values of a microscaled tensor, [rows, k] (ifx_mx4_dequantize)."""
+    device = _on_device(q.codes, q.scales, out)
+    _mx4_check(q, "q")
+    if out is None:
+        out = _alloc((q.rows, q.k), dtype, device, stream)
+    rows, k, ld = _pitch(out)
+    if (rows, k) != (q.rows, q.k):
+        raise ValueError(f"out of {rows} x {k}, q of {q.rows} x {q.k}")
+    _check(lib().ifx_mx4_dequantize(_ptr(q.codes), _ptr(q.scales), rows, k, _ptr(out), _type(out.dtype), ld,
+                                    _stream(stream)), "ifx_mx4_dequantize")
+    return out
+
+
+def mx4_matmul(a: Mx4, w: Mx4, bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+               act: int = ACT_NONE, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """act(a @ w.T + bias + residual), [a.rows, w.rows] (ifx_mx4_matmul); bias float32 [w.rows],
+    residual of the output's type and shape."""
+    device = _on_device(a.codes, a.scales, w.codes, w.scales, bias, residual, out)
+    _mx4_check(a, "a")
+    _mx4_check(w, "w")
+    if a.k != w.k:
+        raise ValueError(f"a of {a.k} columns, w of {w.k}")
+    m, n = a.rows, w.rows
+    _param(bias, n, "bias")
+    if out is None:
+        out = _alloc((m, n), dtype, device, stream)
+    ld_res = n
+    for t in (out, residual):
+        if t is not None and (tuple(t.shape) != (m, n) or t.dtype != out.dtype):
+            raise ValueError(f"out and residual of shape ({m}, {n}) and one type expected")
+    if residual is not None:
+        ld_res = _pitch(residual)[2]
+    d = Mx4Desc(m, n, a.k, _type(out.dtype), act, _pitch(out)[2], ld_res)
+    _check(lib().ifx_mx4_matmul(ctypes.byref(d), _ptr(a.codes), _ptr(a.scales), _ptr(w.codes), _ptr(w.scales),
+                                _ptr(bias), _ptr(residual), _ptr(out), _stream(stream)), "ifx_mx4_matmul")
+    return out
+
+
+def _gn_desc(x: torch.Tensor, groups: int, act: int, eps: float) -> GnDesc:
+    if x.dim() < 2:
+        raise ValueError("x of shape [n, ..., c] expected")
+    n, c = x.shape[0], x.shape[-1]
+    hw = 1
+    for size in x.shape[1:-1]:
+        hw *= size
+    ld = _pitch(x)[2]
+    return GnDesc(n, hw, c, groups, _type(x.dtype), act, float(eps), ld, ld, ld)
+
+
+def _gn_ws(d: GnDesc, backward: int, device, stream):
+    nbytes = lib().ifx_group_norm_workspace_bytes(ctypes.byref(d), backward)
+    return (_alloc((nbytes,), torch.uint8, device, stream) if nbytes else None), nbytes
+
+
+def _gn_stats(x, groups, device, stream):
+    return [_alloc((x.shape[0], max(groups, 0)), torch.float32, device, stream) for _ in range(2)]
+
+
+def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError(f"{name}: shape {tuple(x.shape)} and {x.dtype} expected")
+    return _pitch(t)[2]
+
+
+def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5, act: int = ACT_NONE,
+               out: Optional[torch.Tensor] = None, stream=None):
+    """Group norm of channels-last x [n, ..., c] with an activation (ifx_group_norm) ->
+    (y, mean [n, groups], rstd [n, groups])."""
+    device = _on_device(x, weight, bias, out)
+    d = _gn_desc(x, groups, act, eps)
+    _param(weight, d.c, "weight")
+    _param(bias, d.c, "bias")
+    if out is None:
+        out = _alloc(x.shape, x.dtype, device, stream)
+    d.ld_y = _like(out, x, "out")
+    mean, rstd = _gn_stats(x, groups, device, stream)
+    ws, nbytes = _gn_ws(d, 0, device, stream)
+    _check(lib().ifx_group_norm(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd),
+                                _ptr(ws), nbytes, _stream(stream)), "ifx_group_norm")
+    return out, mean, rstd
+
+
+def group_norm_mx4(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, eps: float = 1e-5, act: int = ACT_NONE,
+                   out: Optional[Mx4] = None, stream=None) -> Mx4:
+    """group_norm whose result is rounded to microscaled 4-bit codes instead of being stored, a row per
+    pixel (ifx_group_norm_mx4)."""
+    device = _on_device(x, weight, bias, *(out[:2] if out is not None else ()))
+    d = _gn_desc(x, groups, act, eps)
+    _param(weight, d.c, "weight")
+    _param(bias, d.c, "bias")
+    if out is None:
+        out = mx4_empty(d.n * d.hw, d.c, device, stream)
+    _mx4_check(out, "out")
+    if (out.rows, out.k) != (d.n * d.hw, d.c):
+        raise ValueError(f"out of {out.rows} x {out.k}, x of {d.n * d.hw} pixels of {d.c} channels")
+    ws, nbytes = _gn_ws(d, 0, device, stream)
+    _check(lib().ifx_group_norm_mx4(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out.codes),
+                                    _ptr(out.scales), None, None, _ptr(ws), nbytes, _stream(stream)),
+           "ifx_group_norm_mx4")
+    return out
+
+
+def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, groups: int,
+                        weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                        act: int = ACT_NONE, out: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of group_norm (ifx_group_norm_backward) -> (dx, dweight [c], dbias [c]); mean and rstd are
+    the forward pass's.  dweight and dbias are float32, also where weight or bias is None (1 and 0)."""
+    device = _on_device(dy, x, mean, rstd, weight, bias, out)
+    d = _gn_desc(x, groups, act, 0.0)
+    _param(weight, d.c, "weight")
+    _param(bias, d.c, "bias")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != torch.float32 or tuple(t.shape) != (d.n, groups) or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous float32 of shape ({d.n}, {groups}) expected")
+    d.ld_dy = _like(dy, x, "dy")
+    if out is None:
+        out = _alloc(x.shape, x.dtype, device, stream)
+    d.ld_y = _like(out, x, "out")
+    dweight, dbias = (_alloc((d.c,), torch.float32, device, stream) for _ in range(2))
+    ws, nbytes = _gn_ws(d, 1, device, stream)
+    _check(lib().ifx_group_norm_backward(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                         _ptr(bias), _ptr(out), _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes,
+                                         _stream(stream)), "ifx_group_norm_backward")
+    return out, dweight, dbias
 
 
 class NetGraph:

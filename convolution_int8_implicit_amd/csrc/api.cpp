@@ -1244,3 +1244,214 @@ int32_t ifx_last_hip_error(void) { return g_last_hip; }
 int32_t ifx_version(void) { return 100; }
 
 }  // extern "C"
+
+// ----------------------------------------------------------------------------
+// Microscaled 4-bit tensors and group norm
+// ----------------------------------------------------------------------------
+namespace {
+
+inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool known_type(int32_t t) { return t == IFX_F32 || t == IFX_BF16 || t == IFX_F16; }
+inline bool known_act(int32_t a) { return a == IFX_ACT_NONE || a == IFX_ACT_RELU || a == IFX_ACT_SILU; }
+inline size_t type_bytes(int32_t t) { return t == IFX_F32 ? 4 : 2; }
+// A tensor of rows every ld elements whose byte offsets fit 63 bits.
+inline bool pitch_ok(int64_t rows, int64_t width, int64_t ld) { return ld >= width && (rows <= 0 || ld <= (1LL << 60) / rows); }
+
+// Rows, columns and grid of a 4-bit tensor.
+ifx_status check_mx4(int32_t rows, int32_t k)
+{
+    if (rows < 0 || k < 1) return IFX_E_SHAPE;
+    const long long tiles = (rows + 15LL) / 16 * ((k + 511LL) / 512);
+    return tiles > 0xffffffffLL / 256 ? IFX_E_SHAPE : IFX_OK;
+}
+
+ifx_status check_codes(const uint8_t *codes, const uint8_t *scales)
+{
+    if (!codes || !scales) return IFX_E_NULL;
+    return aligned16(codes) && aligned_to(scales, 4) ? IFX_OK : IFX_E_ALIGN;
+}
+
+ifx_status check_mx4_rows(const void *x, int32_t type, int64_t ld, int32_t rows, int32_t k, const uint8_t *codes,
+                          const uint8_t *scales)
+{
+    if (!known_type(type)) return IFX_E_UNSUPPORTED;
+    ifx_status st = check_mx4(rows, k);
+    if (st != IFX_OK) return st;
+    if (!pitch_ok(rows, k, ld)) return IFX_E_SHAPE;
+    if (rows == 0) return IFX_OK;
+    if (!x) return IFX_E_NULL;
+    st = check_codes(codes, scales);
+    if (st != IFX_OK) return st;
+    return aligned_to(x, type_bytes(type)) ? IFX_OK : IFX_E_ALIGN;
+}
+
+ifx_status check_gn(const ifx_gn_desc *d, bool backward, bool mx4)
+{
+    if (!d) return IFX_E_NULL;
+    if (!known_type(d->type) || !known_act(d->act)) return IFX_E_UNSUPPORTED;
+    if (d->n < 0 || d->hw < 1 || d->c < 1 || d->groups < 1 || d->c % d->groups || !(d->eps >= 0.0f)) return IFX_E_SHAPE;
+    const int64_t rows = (int64_t)d->n * d->hw;
+    if (!pitch_ok(rows, d->c, d->ld_x) || (!mx4 && !pitch_ok(rows, d->c, d->ld_y))) return IFX_E_SHAPE;
+    if (backward && !pitch_ok(rows, d->c, d->ld_dy)) return IFX_E_SHAPE;
+    if (d->hw > 0x3fffffff || (mx4 && rows > 0x7fffffffLL)) return IFX_E_SHAPE;
+    return ifx::gn_supported(d->n, d->hw, d->c) ? IFX_OK : IFX_E_UNSUPPORTED;
+}
+
+// What the three group norm calls share: the descriptor, x, the parameters, mean and rstd, the workspace.
+ifx_status check_gn_call(const ifx_gn_desc *d, bool backward, bool mx4, const void *x, const float *weight,
+                         const float *bias, const float *mean, const float *rstd, const void *ws, size_t ws_bytes)
+{
+    const ifx_status st = check_gn(d, backward, mx4);
+    if (st != IFX_OK) return st;
+    if (d->n == 0) return IFX_OK;
+    if (!x || (backward && (!mean || !rstd))) return IFX_E_NULL;
+    if (!aligned_to(x, type_bytes(d->type)) || !aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(mean, 4) ||
+        !aligned_to(rstd, 4) || !aligned16(ws))
+        return IFX_E_ALIGN;
+    const size_t need = ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, backward);
+    if (need > ws_bytes) return IFX_E_WORKSPACE;
+    return need > 0 && !ws ? IFX_E_NULL : IFX_OK;
+}
+
+ifx::GnArgs gn_args(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias, void *ws)
+{
+    ifx::GnArgs a = {};
+    a.x = x;
+    a.weight = weight;
+    a.bias = bias;
+    a.ws = (float *)ws;
+    a.n = d->n;
+    a.hw = d->hw;
+    a.c = d->c;
+    a.groups = d->groups;
+    a.type = d->type;
+    a.act = d->act;
+    a.eps = d->eps;
+    a.ld_x = d->ld_x;
+    a.ld_y = d->ld_y;
+    a.ld_dy = d->ld_dy;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ifx_mx4_code_bytes(int32_t rows, int32_t k)
+{
+    return check_mx4(rows, k) == IFX_OK ? (size_t)((k + 127LL) / 128) * rows * 64 : 0;
+}
+
+size_t ifx_mx4_scale_bytes(int32_t rows, int32_t k)
+{
+    return check_mx4(rows, k) == IFX_OK ? (size_t)((k + 127LL) / 128) * rows * 4 : 0;
+}
+
+ifx_status ifx_mx4_quantize(const void *x, int32_t type, int64_t ld, int32_t rows, int32_t k, uint8_t *codes,
+                            uint8_t *scales, void *stream)
+{
+    const ifx_status st = check_mx4_rows(x, type, ld, rows, k, codes, scales);
+    if (st != IFX_OK || rows == 0) return st;
+    return hip_status(ifx::launch_mx4_quantize(x, type, ld, rows, k, codes, scales, (hipStream_t)stream));
+}
+
+ifx_status ifx_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t k, void *y,
+                              int32_t type, int64_t ld, void *stream)
+{
+    const ifx_status st = check_mx4_rows(y, type, ld, rows, k, codes, scales);
+    if (st != IFX_OK || rows == 0) return st;
+    return hip_status(ifx::launch_mx4_dequantize(codes, scales, rows, k, y, type, ld, (hipStream_t)stream));
+}
+
+ifx_status ifx_mx4_matmul(const ifx_mx4_desc *d, const uint8_t *a_codes, const uint8_t *a_scales,
+                          const uint8_t *w_codes, const uint8_t *w_scales, const float *bias, const void *residual,
+                          void *y, void *stream)
+{
+    if (!d) return IFX_E_NULL;
+    if (!known_type(d->type) || !known_act(d->act)) return IFX_E_UNSUPPORTED;
+    if (d->m < 0 || d->n < 0) return IFX_E_SHAPE;
+    ifx_status st = check_mx4(d->m, d->k);
+    if (st == IFX_OK) st = check_mx4(d->n, d->k);
+    if (st != IFX_OK) return st;
+    if (!pitch_ok(d->m, d->n, d->ld_y) || (residual && !pitch_ok(d->m, d->n, d->ld_res))) return IFX_E_SHAPE;
+    if (d->m == 0 || d->n == 0) return IFX_OK;
+    if (!y) return IFX_E_NULL;
+    st = check_codes(a_codes, a_scales);
+    if (st == IFX_OK) st = check_codes(w_codes, w_scales);
+    if (st != IFX_OK) return st;
+    const size_t e = type_bytes(d->type);
+    if (!aligned_to(y, e) || !aligned_to(residual, e) || !aligned_to(bias, 4)) return IFX_E_ALIGN;
+    ifx::Mx4Args a = {};
+    a.a_codes = a_codes;
+    a.a_scales = a_scales;
+    a.w_codes = w_codes;
+    a.w_scales = w_scales;
+    a.bias = bias;
+    a.res = residual;
+    a.y = y;
+    a.m = d->m;
+    a.n = d->n;
+    a.k1 = (d->k - 1) / 128 + 1;
+    a.type = d->type;
+    a.act = d->act;
+    a.ld_y = d->ld_y;
+    a.ld_res = d->ld_res;
+    return hip_status(ifx::launch_mx4_matmul(a, (hipStream_t)stream));
+}
+
+size_t ifx_group_norm_workspace_bytes(const ifx_gn_desc *d, int32_t backward)
+{
+    if (check_gn(d, backward != 0, false) != IFX_OK) return 0;
+    return ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, backward != 0);
+}
+
+ifx_status ifx_group_norm(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias, void *y,
+                          float *mean, float *rstd, void *ws, size_t ws_bytes, void *stream)
+{
+    const ifx_status st = check_gn_call(d, false, false, x, weight, bias, mean, rstd, ws, ws_bytes);
+    if (st != IFX_OK || d->n == 0) return st;
+    if (!y) return IFX_E_NULL;
+    if (!aligned_to(y, type_bytes(d->type))) return IFX_E_ALIGN;
+    ifx::GnArgs a = gn_args(d, x, weight, bias, ws);
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    return hip_status(ifx::launch_group_norm(a, (hipStream_t)stream));
+}
+
+ifx_status ifx_group_norm_mx4(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias,
+                              uint8_t *codes, uint8_t *scales, float *mean, float *rstd, void *ws, size_t ws_bytes,
+                              void *stream)
+{
+    ifx_status st = check_gn_call(d, false, true, x, weight, bias, mean, rstd, ws, ws_bytes);
+    if (st != IFX_OK || d->n == 0) return st;
+    st = check_codes(codes, scales);
+    if (st != IFX_OK) return st;
+    ifx::GnArgs a = gn_args(d, x, weight, bias, ws);
+    a.codes = codes;
+    a.scales = scales;
+    a.mean = mean;
+    a.rstd = rstd;
+    return hip_status(ifx::launch_group_norm(a, (hipStream_t)stream));
+}
+
+ifx_status ifx_group_norm_backward(const ifx_gn_desc *d, const void *dy, const void *x, const float *mean,
+                                   const float *rstd, const float *weight, const float *bias, void *dx,
+                                   float *dweight, float *dbias, void *ws, size_t ws_bytes, void *stream)
+{
+    const ifx_status st = check_gn_call(d, true, false, x, weight, bias, mean, rstd, ws, ws_bytes);
+    if (st != IFX_OK) return st;
+    if (!aligned_to(dweight, 4) || !aligned_to(dbias, 4)) return IFX_E_ALIGN;
+    if (d->n > 0) {
+        if (!dy || !dx) return IFX_E_NULL;
+        if (!aligned_to(dy, type_bytes(d->type)) || !aligned_to(dx, type_bytes(d->type))) return IFX_E_ALIGN;
+    }
+    ifx::GnArgs a = gn_args(d, x, weight, bias, ws);
+    a.dy = dy;
+    a.y = dx;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    return hip_status(ifx::launch_group_norm_grad(a, dweight, dbias, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -141,6 +141,37 @@ struct FoldArgs {
     const float *w_scale, *conv_bias, *gamma, *beta, *mean, *var;
 };
 
+// One product of two microscaled 4-bit tensors (device pointers; see ifx_mx4_matmul).
+struct Mx4Args {
+    const uint8_t *a_codes, *a_scales;  // [k1][m][64], [k1][m][4]
+    const uint8_t *w_codes, *w_scales;  // [k1][n][64], [k1][n][4]
+    const float *bias;                  // [n] or null
+    const void *res;                    // rows of n every ld_res elements, of `type`, or null
+    void *y;                            // rows of n every ld_y elements, of `type`
+    int m, n, k1;
+    int type, act;
+    long long ld_y, ld_res;
+};
+
+// One group norm or its gradient (device pointers; see ifx_group_norm).
+struct GnArgs {
+    const void *x, *dy;
+    void *y;                     // y, or dx of the gradient
+    uint8_t *codes, *scales;     // instead of y: microscaled 4-bit codes (else null)
+    const float *weight, *bias;  // [c] or null
+    float *mean, *rstd;          // [n][groups]; written by the forward pass (or null), read by the gradient
+    float *ws, *gsum;
+    int n, hw, c, groups;
+    int type, act;
+    float eps;
+    long long ld_x, ld_dy, ld_y;
+    // set by the launcher: channels of a group and their division, lanes that sum one group,
+    // chunks of a sample and their pixels
+    int cg, cg_shr;
+    unsigned cg_mul;
+    int lpg, chunks, px;
+};
+
 hipError_t launch_conv(const ConvArgs &a, int kh, int kw, hipStream_t s);
 // Whether the kernel launch_conv_split picks for `a` honours a.in_ps / a.out_ps (the general
 // kernel does; a launch it would split over K is not given a phase-split output).
@@ -159,6 +190,17 @@ hipError_t launch_conv_proj(const ConvArgs &a, const ConvArgs &pj, hipStream_t s
 hipError_t launch_quantize(const void *x, bool u8, int8_t *q, int count, int c, const float *mean, const float *mult,
                            hipStream_t s);
 hipError_t launch_dequantize(const int32_t *q, float *y, int count, float scale, hipStream_t s);
+// microscaled 4-bit rounding and product, mx4.hip
+hipError_t launch_mx4_quantize(const void *x, int type, long long ld, int rows, int k, uint8_t *codes, uint8_t *scales,
+                               hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int k, void *y, int type,
+                                 long long ld, hipStream_t s);
+hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s);
+// group norm with an activation and its gradient, norm.hip
+bool gn_supported(int n, int hw, int c);
+size_t gn_workspace_bytes(int n, int hw, int c, int groups, bool grad);
+hipError_t launch_group_norm(GnArgs a, hipStream_t s);
+hipError_t launch_group_norm_grad(GnArgs a, float *dweight, float *dbias, hipStream_t s);
 hipError_t launch_fold_bn(const FoldArgs &f, int32_t *bias, int32_t *mult, int32_t *shift, int32_t *status,
                           hipStream_t s);
 // 1x1 convolutions with at most 128 input channels (conv1x1.hip)

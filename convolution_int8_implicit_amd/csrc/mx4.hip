@@ -1,0 +1,184 @@
+// Microscaled 4-bit floating point: rounding, the values back, and the product of two such tensors.
+//
+// A tensor of `rows` rows and k columns holds blocks of 32 consecutive columns of a row: 4-bit
+// codes (sign, two exponent bits, one mantissa bit; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one
+// power of two per block, 2^(s - 127) with the byte s (255: NaN).  The layout is blocked by
+// 128 columns as the int8 activations are by 32 channels: codes [K1][rows][64] bytes and scales
+// [K1][rows][4] bytes, K1 = ceil(k / 128), columns past k zero.  128 columns are what one wave's
+// matrix instruction reads (16 rows) or what two read (32 rows), so a step of a product over
+// any run of rows is one contiguous run of codes and one of scales.
+#include "device_common.h"
+#include "ifx_internal.h"
+#include "lowp.h"
+
+namespace ifx {
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+constexpr int kFp4 = 4;  // the matrix instruction's operand format: 4-bit e2m1
+
+__device__ __forceinline__ v8i wide(v4i x) { return (v8i){x[0], x[1], x[2], x[3], 0, 0, 0, 0}; }
+
+// ------------------------------------------------------------------------------------------
+// Rounding.  Streaming, HBM-bound: a thread rounds eight consecutive columns (one 16-byte load of
+// a 16-bit type), four threads a block, sixteen a row's 128-column panel, so a workgroup covers
+// 16 rows of a panel: 64-byte codes of 16 consecutive rows are a contiguous kilobyte of the
+// output.  Four panels per workgroup keep four loads in flight per thread.
+// ------------------------------------------------------------------------------------------
+constexpr int kQRows = 16, kQPanels = 4;
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *x, long long ld, int rows, int k, int k1,
+                                                           int groups, uint8_t *codes, uint8_t *scales)
+{
+    typedef typename Elem<TYPE>::type E;
+    const int rt = (int)(blockIdx.x / (unsigned)groups), pg = (int)(blockIdx.x - (unsigned)rt * (unsigned)groups);
+    const int t = threadIdx.x, v = t & 15;
+    const int row = rt * kQRows + (t >> 4);
+    const bool live = row < rows;
+    const E *src = (const E *)x + (long long)(live ? row : rows - 1) * ld;
+    E raw[kQPanels][8];
+#pragma unroll
+    for (int i = 0; i < kQPanels; ++i) {
+        const int col = (pg * kQPanels + i) * 128 + v * 8;
+        load8(src + (col < k ? col : 0), k - col < 0 ? 0 : k - col, raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kQPanels; ++i) {
+        const int p = pg * kQPanels + i;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (float)raw[i][e];
+        unsigned s;
+        const unsigned r = mx4_codes(f, s);
+        if (live && p < k1) {
+            const long long at = (long long)p * rows + row;
+            ((unsigned *)codes)[at * 16 + v] = r;
+            if ((v & 3) == 0) scales[at * 4 + (v >> 2)] = (uint8_t)s;
+        }
+    }
+}
+
+// The values back: eight columns per thread, 4 bytes of codes in, one 16-byte store of a 16-bit
+// type out.  Every value of a finite block is exact in bfloat16.
+template <int TYPE>
+__global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *codes, const uint8_t *scales, int rows,
+                                                             int k, int k1, int groups, void *y, long long ld)
+{
+    typedef typename Elem<TYPE>::type E;
+    const int rt = (int)(blockIdx.x / (unsigned)groups), pg = (int)(blockIdx.x - (unsigned)rt * (unsigned)groups);
+    const int t = threadIdx.x, v = t & 15;
+    const int row = rt * kQRows + (t >> 4);
+    if (row >= rows) return;
+    unsigned c[kQPanels], s[kQPanels];
+#pragma unroll
+    for (int i = 0; i < kQPanels; ++i) {
+        const int p = pg * kQPanels + i;
+        const long long at = (long long)(p < k1 ? p : k1 - 1) * rows + row;
+        c[i] = ((const unsigned *)codes)[at * 16 + v];
+        s[i] = scales[at * 4 + (v >> 2)];
+    }
+#pragma unroll
+    for (int i = 0; i < kQPanels; ++i) {
+        const int col = (pg * kQPanels + i) * 128 + v * 8;
+        if (col >= k) break;
+        const float sf = __uint_as_float(s[i] << 23);
+        float f[8];
+        auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sf, 0);
+        auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sf, 1);
+        auto d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sf, 2);
+        auto e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sf, 3);
+        f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1], f[4] = d[0], f[5] = d[1], f[6] = e[0], f[7] = e[1];
+        store8((E *)y + (long long)row * ld + col, k - col, f);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// Product y[m, n] = act(sum_k A[m, k] W[n, k] + bias[n] + residual[m, n]).
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ float load_any(const void *p, int type, long long i)
+{
+    return type == 0 ? ((const float *)p)[i] : type == 1 ? (float)((const __bf16 *)p)[i] : (float)((const _Float16 *)p)[i];
+}
+__device__ __forceinline__ void store_any(void *p, int type, long long i, float f)
+{
+    if (type == 0)
+        ((float *)p)[i] = f;
+    else if (type == 1)
+        ((__bf16 *)p)[i] = (__bf16)f;
+    else
+        ((_Float16 *)p)[i] = (_Float16)f;
+}
+
+// Few rows: a workgroup of WAVES waves takes 16 weight rows and 16 rows of A; wave w multiplies
+// panels w, w + WAVES, ... straight from memory (16 rows of a panel are one contiguous kilobyte,
+// one 16-byte load per lane) and the partial sums meet in LDS, summed in wave order.
+// The 16x16x128 instruction takes row l % 16 and columns 32 (l / 16) .. + 31 from lane l, one
+// block with its scale in the lowest byte; lane l's results are column l % 16 (a row of A here)
+// and rows 4 (l / 16) .. + 3 (weight rows).
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void mx4_rows_kernel(Mx4Args a, int tiles_n)
+{
+    __shared__ float part[WAVES][256];
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63, c = l & 15, g = l >> 4;
+    const unsigned tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x - tm * (unsigned)tiles_n;
+    const int m0 = (int)tm * 16, n0 = (int)tn * 16;
+    const int ar = min(m0 + c, a.m - 1), wr = min(n0 + c, a.n - 1);
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = w; p < a.k1; p += WAVES) {
+        const long long ai = (long long)p * a.m + ar, wi = (long long)p * a.n + wr;
+        const v4i av = ((const v4i *)a.a_codes)[ai * 4 + g];
+        const v4i wv = ((const v4i *)a.w_codes)[wi * 4 + g];
+        const int as = a.a_scales[ai * 4 + g], ws = a.w_scales[wi * 4 + g];
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(wv), wide(av), acc, kFp4, kFp4, 0, ws, 0, as);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[w][c * 16 + 4 * g + i] = acc[i];
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < 256) {
+        float f = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) f += part[i][t];
+        const int m = m0 + (t >> 4), n = n0 + (t & 15);
+        if (m < a.m && n < a.n) {
+            if (a.bias) f += a.bias[n];
+            if (a.res) f += load_any(a.res, a.type, (long long)m * a.ld_res + n);
+            store_any(a.y, a.type, (long long)m * a.ld_y + n, act_any(a.act, f));
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(const void *x, int type, long long ld, int rows, int k, uint8_t *codes, uint8_t *scales,
+                               hipStream_t s)
+{
+    const int k1 = (k + 127) / 128, groups = (k1 + kQPanels - 1) / kQPanels;
+    const dim3 grid((unsigned)((rows + kQRows - 1LL) / kQRows * groups));
+    auto *f = type == 0 ? mx4_quantize_kernel<0> : type == 1 ? mx4_quantize_kernel<1> : mx4_quantize_kernel<2>;
+    hipLaunchKernelGGL(f, grid, dim3(256), 0, s, x, ld, rows, k, k1, groups, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int k, void *y, int type,
+                                 long long ld, hipStream_t s)
+{
+    const int k1 = (k + 127) / 128, groups = (k1 + kQPanels - 1) / kQPanels;
+    const dim3 grid((unsigned)((rows + kQRows - 1LL) / kQRows * groups));
+    auto *f = type == 0 ? mx4_dequantize_kernel<0> : type == 1 ? mx4_dequantize_kernel<1> : mx4_dequantize_kernel<2>;
+    hipLaunchKernelGGL(f, grid, dim3(256), 0, s, codes, scales, rows, k, k1, groups, y, ld);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s)
+{
+    const int tiles_n = (a.n + 15) / 16;
+    const dim3 grid((unsigned)((a.m + 15LL) / 16 * tiles_n));
+    hipLaunchKernelGGL(mx4_rows_kernel<8>, grid, dim3(512), 0, s, a, tiles_n);
+    return hipGetLastError();
+}
+
+}  // namespace ifx

@@ -27,7 +27,9 @@
  *   - Arguments are validated on the host before anything is launched.  On
  *     an error status nothing has been enqueued.  Validation touches no
  *     device, so every error path runs without a GPU.
- *   - All arithmetic is integer; results are deterministic and bit-exact.
+ *   - All arithmetic of the int8 path is integer; results are deterministic
+ *     and bit-exact.  The 4-bit and group norm entry points at the end of this
+ *     file compute in 32-bit floating point; they too are deterministic.
  *
  * Layouts (Inspur conv-merge article, section 3.1):
  *   activation  NC/32HW32: [N, C1=ceil(C/32), H, W, 32] int8; channel c of
@@ -451,6 +453,122 @@ ifx_status ifx_quantize_u8(const uint8_t *x, int8_t *q, int64_t count, int32_t c
  * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN.
  */
 ifx_status ifx_dequantize_i32(const int32_t *q, float *y, int64_t count, float scale, void *stream);
+
+/* Element types and activations of the 4-bit and group norm entry points. */
+enum { IFX_F32 = 0, IFX_BF16 = 1, IFX_F16 = 2 };
+enum { IFX_ACT_NONE = 0, IFX_ACT_RELU = 1, IFX_ACT_SILU = 2 }; /* z, max(z, 0), z / (1 + e^-z) */
+
+/*
+ * Microscaled 4-bit floating point.  A tensor of `rows` rows and k columns
+ * holds blocks of 32 consecutive columns of a row: a code of 4 bits per column
+ * (sign, two exponent bits, one mantissa bit; magnitudes 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6) and one byte s per block; a column's value is code * 2^(s - 127), NaN
+ * where s is 255.  Layout, blocked by 128 columns, K1 = ceil(k / 128):
+ *   codes   [K1, rows, 64] uint8: column 128 i + 2 j in the low four bits of
+ *           byte [i, row, j], column 128 i + 2 j + 1 in the high four
+ *   scales  [K1, rows, 4] uint8: the block of columns 128 i + 32 b .. + 31 at
+ *           [i, row, b]
+ * Codes of columns past k are 0 and their scales are not 255 (ifx_mx4_quantize
+ * and ifx_group_norm_mx4 write 0 there); the product relies on it.
+ *
+ * ifx_mx4_quantize rounds a block x to it:
+ *   s    = max(0, floor(log2 max |x|) + 125)      (0 for a block of zeros)
+ *   code = x / 2^(s - 127) rounded to the nearest magnitude, halves to the
+ *          even code, at most 6
+ * (values from 6.0 up to 8.0 units saturate).  A block that holds a NaN or an
+ * infinity gets s = 255 and zero codes.  ifx_mx4_dequantize writes the values:
+ * exact in IFX_F32 and IFX_BF16 from s = 0 to 252, one rounding in IFX_F16.
+ *   x, y    DEVICE, rows of k elements of `type`, one every ld >= k elements;
+ *           aligned to the element (rows need no more alignment than that)
+ *   codes   DEVICE, ifx_mx4_code_bytes, 16-byte aligned
+ *   scales  DEVICE, ifx_mx4_scale_bytes, 4-byte aligned
+ *   rows    >= 0 (0: nothing to do, pointers are not looked at); k >= 1;
+ *           at most 2^32 / 256 tiles of 16 rows and 512 columns
+ * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN and
+ * IFX_E_UNSUPPORTED for an unknown type.
+ */
+size_t ifx_mx4_code_bytes(int32_t rows, int32_t k);  /* host-only; 0 for a bad shape */
+size_t ifx_mx4_scale_bytes(int32_t rows, int32_t k); /* host-only; 0 for a bad shape */
+
+ifx_status ifx_mx4_quantize(const void *x, int32_t type, int64_t ld, int32_t rows, int32_t k, uint8_t *codes,
+                            uint8_t *scales, void *stream);
+ifx_status ifx_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t k, void *y,
+                              int32_t type, int64_t ld, void *stream);
+
+/*
+ * Product of two such tensors, A of m rows and W of n rows, both of k columns
+ * (a 1x1 convolution over m pixels, or a linear layer):
+ *   y[i, j] = act(sum_c A[i, c] W[j, c] + bias[j] + residual[i, j])
+ * accumulated in 32-bit floating point on the 4-bit matrix units and rounded
+ * once to `type`.  The sum of one (m, n, k) is taken in one order, so results
+ * are the same from call to call.  A NaN block makes its row of y (A) or its
+ * column (W) NaN.
+ *   bias      DEVICE float32 [n], 4-byte aligned, or NULL
+ *   residual  DEVICE, m rows of n elements of `type`, one every ld_res >= n
+ *             elements, element-aligned, or NULL; may be y itself (same pitch)
+ *   y         DEVICE, m rows of n elements of `type`, one every ld_y >= n
+ *             elements, element-aligned; no other operand may overlap it
+ *   m, n      >= 0 (either 0: nothing to do); k >= 1
+ * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN,
+ * IFX_E_UNSUPPORTED (type, act).
+ */
+typedef struct {
+    int32_t m, n, k;
+    int32_t type, act;
+    int64_t ld_y, ld_res;
+} ifx_mx4_desc;
+
+ifx_status ifx_mx4_matmul(const ifx_mx4_desc *d, const uint8_t *a_codes, const uint8_t *a_scales,
+                          const uint8_t *w_codes, const uint8_t *w_scales, const float *bias, const void *residual,
+                          void *y, void *stream);
+
+/*
+ * Group norm with an activation, channels last.  x is n samples of hw pixels
+ * of c channels; a pixel lies every ld_x elements (>= c), a sample every
+ * hw * ld_x.  Group j of a sample is its channels j * c / groups .. of every
+ * pixel; with the group's mean and (biased) variance:
+ *   xhat = (x - mean) * rstd,  rstd = 1 / sqrt(var + eps)
+ *   y    = act(xhat * weight + bias)
+ * ifx_group_norm writes y (one rounding to `type`); ifx_group_norm_mx4 rounds
+ * the same 32-bit values, unrounded in between, to microscaled 4-bit codes:
+ * rows are the n * hw pixels, columns the channels (codes and scales as
+ * ifx_mx4_quantize lays them out).  Both write mean and rstd, float32
+ * [n, groups], where the pointers are not NULL.  With the gradient dy of y,
+ * dz = dy act'(xhat weight + bias) (for ReLU 0 where that is <= 0) and
+ * d = dz * weight, ifx_group_norm_backward writes
+ *   dx      = rstd * (d - mean(d) - xhat * mean(d * xhat))   (to `type`)
+ *   dweight = sum over samples and pixels of dz * xhat,  dbias = sum of dz
+ * from the forward pass's mean and rstd.  dweight or dbias may be NULL.
+ *   x, y, dy, dx  DEVICE, of `type`, element-aligned, pitches ld_x, ld_y (y
+ *                 or dx) and ld_dy (the gradient only).  y may be x and dx may
+ *                 be x or dy (same pitch)
+ *   weight, bias  DEVICE float32 [c], 4-byte aligned, or NULL (1 and 0)
+ *   dweight, dbias, mean, rstd  DEVICE float32, 4-byte aligned
+ *   n >= 0, hw >= 1, 1 <= c <= 8192, groups >= 1 dividing c, eps >= 0
+ *   ws            DEVICE, 16-byte aligned, at least
+ *                 ifx_group_norm_workspace_bytes (may be NULL where that is 0)
+ * With n = 0 nothing is read and only dweight and dbias are written (zeros).
+ * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN,
+ * IFX_E_WORKSPACE, IFX_E_UNSUPPORTED (type, act, c > 8192).
+ */
+typedef struct {
+    int32_t n, hw, c, groups;
+    int32_t type, act;
+    float eps;
+    int64_t ld_x, ld_y, ld_dy;
+} ifx_gn_desc;
+
+/* Host-only: workspace bytes of the forward calls (backward 0) or the gradient (1); 0 for a bad desc. */
+size_t ifx_group_norm_workspace_bytes(const ifx_gn_desc *d, int32_t backward);
+
+ifx_status ifx_group_norm(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias, void *y,
+                          float *mean, float *rstd, void *ws, size_t ws_bytes, void *stream);
+ifx_status ifx_group_norm_mx4(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias,
+                              uint8_t *codes, uint8_t *scales, float *mean, float *rstd, void *ws, size_t ws_bytes,
+                              void *stream);
+ifx_status ifx_group_norm_backward(const ifx_gn_desc *d, const void *dy, const void *x, const float *mean,
+                                   const float *rstd, const float *weight, const float *bias, void *dx,
+                                   float *dweight, float *dbias, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Host-only: the kernel instance ifx_conv_fused(d, ...) launches, named as
