@@ -196,6 +196,7 @@ hipError_t launch_mx4_quantize(const void *x, int type, long long ld, int rows, 
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int k, void *y, int type,
                                  long long ld, hipStream_t s);
 hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s);
+hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s);  // its tiled form, mx4_gemm.hip
 // group norm with an activation and its gradient, norm.hip
 bool gn_supported(int n, int hw, int c);
 size_t gn_workspace_bytes(int n, int hw, int c, int groups, bool grad);

@@ -175,6 +175,7 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
 
 hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s)
 {
+    if (a.m > 64) return launch_mx4_tiles(a, s);
     const int tiles_n = (a.n + 15) / 16;
     const dim3 grid((unsigned)((a.m + 15LL) / 16 * tiles_n));
     hipLaunchKernelGGL(mx4_rows_kernel<8>, grid, dim3(512), 0, s, a, tiles_n);

@@ -267,7 +267,9 @@ def check_product(y, m, n, k, a, w, bias, res, act, kind):
 
 
 SHAPES = [(1, 1, 1), (1, 40, 2048), (2, 17, 33), (5, 1000, 130), (16, 16, 128), (17, 31, 129), (33, 65, 640),
-          (64, 64, 256), (65, 130, 96), (100, 300, 1000), (130, 257, 385), (257, 129, 512), (300, 520, 64)]
+          (64, 64, 256), (65, 130, 96), (100, 300, 1000), (130, 257, 385), (257, 129, 512), (300, 520, 64),
+          # enough tiles for the larger ones, edges inside a tile, one to seven steps of the ring
+          (2050, 2049, 300), (2111, 1930, 900), (4097, 4100, 130), (4200, 3970, 600)]
 
 
 @pytest.mark.gpu
