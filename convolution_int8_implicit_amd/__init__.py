@@ -459,35 +459,50 @@ def fold_bn(x_scale: float, y_scale: float, eps: float, w_scale: torch.Tensor, g
 # ---------------------------------------------------------------------------
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
+# The raw handle of a device's current stream, without a torch.cuda.Stream object around it (these calls are
+# a few microseconds long).
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _type(dtype: torch.dtype) -> int:
-    if dtype not in _TYPES:
+    t = _TYPES.get(dtype)
+    if t is None:
         raise TypeError(f"float32, bfloat16 or float16 expected, not {dtype}")
-    return _TYPES[dtype]
+    return t
 
 
-def _on_device(*ts) -> torch.device:
+def _on_device(*ts) -> int:
     """The device of the tensors given: one GPU, the current one (the library launches there)."""
-    devices = {t.device for t in ts if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError(f"tensors of one GPU expected, not {sorted(map(str, devices))}")
-    device = devices.pop()
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return device
+    index = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors of one GPU expected, not {sorted({str(t.device) for t in ts if t is not None})}")
+    if index < 0:
+        raise ValueError("tensors of a GPU expected")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{torch.cuda.current_device()}")
+    return index
+
+
+def _raw_stream(stream, index: int) -> int:
+    if stream is None:
+        return _current_raw(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _pitch(t: torch.Tensor):
     """(rows, columns, elements from row to row) of a tensor whose last axis is contiguous and whose
     other axes step as one: a contiguous tensor, or a slice of the last axis of one."""
-    if t.dim() == 0:
+    shape = t.shape
+    if not shape:
         raise ValueError("a tensor of one or more axes expected")
-    k = t.shape[-1]
-    if t.numel() == 0:
+    k = shape[-1]
+    if t.is_contiguous():
         return t.numel() // k if k else 0, k, k
     rows, ld = 1, None
     ok = k == 1 or t.stride(-1) == 1
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if ld is None:
@@ -495,23 +510,27 @@ def _pitch(t: torch.Tensor):
         ok = ok and stride == ld * rows
         rows *= size
     ld = k if ld is None else ld
-    if not ok or ld < k:
-        raise ValueError(f"rows of shape {tuple(t.shape)} and strides {t.stride()} do not lie at one pitch")
-    return rows, k, ld
+    if t.numel() and (not ok or ld < k):
+        raise ValueError(f"rows of shape {tuple(shape)} and strides {t.stride()} do not lie at one pitch")
+    return rows, k, max(ld, k)
 
 
-def _alloc(shape, dtype, device, stream) -> torch.Tensor:
-    """Uninitialised memory that belongs to the stream that will use it."""
+def _alloc(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """Uninitialised memory on the device of `like` that belongs to the stream that will use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _param(t: Optional[torch.Tensor], n: int, name: str) -> None:
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+    if t is not None and (t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous()):
         raise ValueError(f"{name}: contiguous float32 of shape ({n},) expected")
 
 
@@ -527,47 +546,59 @@ class Mx4(NamedTuple):
         return self.codes.shape[1]
 
 
-def mx4_empty(rows: int, k: int, device="cuda", stream=None) -> Mx4:
+def _mx4_like(rows: int, k: int, like: torch.Tensor, stream) -> Mx4:
     k1 = (k + 127) // 128
-    return Mx4(_alloc((k1, rows, 64), torch.uint8, device, stream), _alloc((k1, rows, 4), torch.uint8, device, stream), k)
+    return Mx4(_alloc((k1, rows, 64), torch.uint8, like, stream), _alloc((k1, rows, 4), torch.uint8, like, stream), k)
 
 
-def _mx4_check(q: Mx4, name: str) -> None:
-    k1 = (q.k + 127) // 128
-    for t, last in ((q.codes, 64), (q.scales, 4)):
-        if t.dtype != torch.uint8 or t.dim() != 3 or t.shape[0] != k1 or t.shape[2] != last or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous uint8 [{k1}, rows, {last}] expected for k = {q.k}")
-    if q.codes.shape[1] != q.scales.shape[1]:
-        raise ValueError(f"{name}: codes and scales of as many rows expected")
+def mx4_empty(rows: int, k: int, device="cuda") -> Mx4:
+    """Uninitialised codes and scales, for the `out` of a call."""
+    k1 = (k + 127) // 128
+    return Mx4(torch.empty((k1, rows, 64), dtype=torch.uint8, device=device),
+               torch.empty((k1, rows, 4), dtype=torch.uint8, device=device), k)
+
+
+def _mx4_check(q: Mx4, name: str) -> int:
+    """The rows of q."""
+    codes, scales, k = q
+    k1 = (k + 127) // 128
+    rows = codes.shape[1] if codes.dim() == 3 else -1
+    if (codes.shape != (k1, rows, 64) or scales.shape != (k1, rows, 4) or codes.dtype != torch.uint8
+            or scales.dtype != torch.uint8 or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError(f"{name}: contiguous uint8 codes [{k1}, rows, 64] and scales [{k1}, rows, 4] expected for k = {k}")
+    return rows
 
 
 def mx4_quantize(x: torch.Tensor, out: Optional[Mx4] = None, stream=None) -> Mx4:
     """x [..., k] (float32, bfloat16 or float16) rounded to microscaled 4-bit codes, a row per leading
     index (ifx_mx4_quantize)."""
-    device = _on_device(x, *(out[:2] if out is not None else ()))
     rows, k, ld = _pitch(x)
     if out is None:
-        out = mx4_empty(rows, k, device, stream)
-    _mx4_check(out, "out")
-    if (out.rows, out.k) != (rows, k):
-        raise ValueError(f"out of {out.rows} x {out.k}, x of {rows} x {k}")
-    _check(lib().ifx_mx4_quantize(_ptr(x), _type(x.dtype), ld, rows, k, _ptr(out.codes), _ptr(out.scales),
-                                  _stream(stream)), "ifx_mx4_quantize")
+        index = _on_device(x)
+        out = _mx4_like(rows, k, x, stream)
+    else:
+        index = _on_device(x, out.codes, out.scales)
+        if _mx4_check(out, "out") != rows or out.k != k:
+            raise ValueError(f"out of {out.rows} x {out.k}, x of {rows} x {k}")
+    _check(lib().ifx_mx4_quantize(x.data_ptr(), _type(x.dtype), ld, rows, k, out.codes.data_ptr(), out.scales.data_ptr(),
+                                  _raw_stream(stream, index)), "ifx_mx4_quantize")
     return out
 
 
 def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:
     """The values of a microscaled tensor, [rows, k] (ifx_mx4_dequantize)."""
-    device = _on_device(q.codes, q.scales, out)
-    _mx4_check(q, "q")
+    index = _on_device(q.codes, q.scales, out)
+    rows, k = _mx4_check(q, "q"), q.k
+    ld = k
     if out is None:
-        out = _alloc((q.rows, q.k), dtype, device, stream)
-    rows, k, ld = _pitch(out)
-    if (rows, k) != (q.rows, q.k):
-        raise ValueError(f"out of {rows} x {k}, q of {q.rows} x {q.k}")
-    _check(lib().ifx_mx4_dequantize(_ptr(q.codes), _ptr(q.scales), rows, k, _ptr(out), _type(out.dtype), ld,
-                                    _stream(stream)), "ifx_mx4_dequantize")
+        out = _alloc((rows, k), dtype, q.codes, stream)
+    else:
+        if out.shape != (rows, k):
+            raise ValueError(f"out of shape {tuple(out.shape)}, q of {rows} x {k}")
+        ld = _pitch(out)[2]
+    _check(lib().ifx_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, k, out.data_ptr(), _type(out.dtype),
+                                    ld, _raw_stream(stream, index)), "ifx_mx4_dequantize")
     return out
 
 
@@ -576,45 +607,43 @@ def mx4_matmul(a: Mx4, w: Mx4, bias: Optional[torch.Tensor] = None, residual: Op
                stream=None) -> torch.Tensor:
     """act(a @ w.T + bias + residual), [a.rows, w.rows] (ifx_mx4_matmul); bias float32 [w.rows],
     residual of the output's type and shape."""
-    device = _on_device(a.codes, a.scales, w.codes, w.scales, bias, residual, out)
-    _mx4_check(a, "a")
-    _mx4_check(w, "w")
+    index = _on_device(a.codes, a.scales, w.codes, w.scales, bias, residual, out)
+    m, n = _mx4_check(a, "a"), _mx4_check(w, "w")
     if a.k != w.k:
         raise ValueError(f"a of {a.k} columns, w of {w.k}")
-    m, n = a.rows, w.rows
     _param(bias, n, "bias")
+    ld_y = ld_res = n
     if out is None:
-        out = _alloc((m, n), dtype, device, stream)
-    ld_res = n
-    for t in (out, residual):
-        if t is not None and (tuple(t.shape) != (m, n) or t.dtype != out.dtype):
-            raise ValueError(f"out and residual of shape ({m}, {n}) and one type expected")
+        out = _alloc((m, n), dtype, a.codes, stream)
+    else:
+        if out.shape != (m, n):
+            raise ValueError(f"out of shape ({m}, {n}) expected")
+        ld_y = _pitch(out)[2]
     if residual is not None:
+        if residual.shape != (m, n) or residual.dtype != out.dtype:
+            raise ValueError(f"residual of shape ({m}, {n}) and {out.dtype} expected")
         ld_res = _pitch(residual)[2]
-    d = Mx4Desc(m, n, a.k, _type(out.dtype), act, _pitch(out)[2], ld_res)
-    _check(lib().ifx_mx4_matmul(ctypes.byref(d), _ptr(a.codes), _ptr(a.scales), _ptr(w.codes), _ptr(w.scales),
-                                _ptr(bias), _ptr(residual), _ptr(out), _stream(stream)), "ifx_mx4_matmul")
+    d = Mx4Desc(m, n, a.k, _type(out.dtype), act, ld_y, ld_res)
+    _check(lib().ifx_mx4_matmul(d, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+                                _addr(bias), _addr(residual), out.data_ptr(), _raw_stream(stream, index)),
+           "ifx_mx4_matmul")
     return out
 
 
 def _gn_desc(x: torch.Tensor, groups: int, act: int, eps: float) -> GnDesc:
     if x.dim() < 2:
         raise ValueError("x of shape [n, ..., c] expected")
-    n, c = x.shape[0], x.shape[-1]
+    ld = _pitch(x)[2]
     hw = 1
     for size in x.shape[1:-1]:
         hw *= size
-    ld = _pitch(x)[2]
-    return GnDesc(n, hw, c, groups, _type(x.dtype), act, float(eps), ld, ld, ld)
+    return GnDesc(x.shape[0], hw, x.shape[-1], groups, _type(x.dtype), act, eps, ld, ld, ld)
 
 
-def _gn_ws(d: GnDesc, backward: int, device, stream):
-    nbytes = lib().ifx_group_norm_workspace_bytes(ctypes.byref(d), backward)
-    return (_alloc((nbytes,), torch.uint8, device, stream) if nbytes else None), nbytes
-
-
-def _gn_stats(x, groups, device, stream):
-    return [_alloc((x.shape[0], max(groups, 0)), torch.float32, device, stream) for _ in range(2)]
+def _gn_ws(d: GnDesc, backward: int, like: torch.Tensor, stream):
+    """The workspace (None where none is needed) and its bytes."""
+    nbytes = lib().ifx_group_norm_workspace_bytes(d, backward)
+    return (_alloc((nbytes,), torch.uint8, like, stream) if nbytes else None), nbytes
 
 
 def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
@@ -628,17 +657,20 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
                out: Optional[torch.Tensor] = None, stream=None):
     """Group norm of channels-last x [n, ..., c] with an activation (ifx_group_norm) ->
     (y, mean [n, groups], rstd [n, groups])."""
-    device = _on_device(x, weight, bias, out)
+    index = _on_device(x, weight, bias, out)
     d = _gn_desc(x, groups, act, eps)
     _param(weight, d.c, "weight")
     _param(bias, d.c, "bias")
     if out is None:
-        out = _alloc(x.shape, x.dtype, device, stream)
-    d.ld_y = _like(out, x, "out")
-    mean, rstd = _gn_stats(x, groups, device, stream)
-    ws, nbytes = _gn_ws(d, 0, device, stream)
-    _check(lib().ifx_group_norm(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd),
-                                _ptr(ws), nbytes, _stream(stream)), "ifx_group_norm")
+        out = _alloc(x.shape, x.dtype, x, stream)
+        d.ld_y = d.c
+    else:
+        d.ld_y = _like(out, x, "out")
+    shape = (d.n, max(groups, 0))
+    mean, rstd = _alloc(shape, torch.float32, x, stream), _alloc(shape, torch.float32, x, stream)
+    ws, nbytes = _gn_ws(d, 0, x, stream)
+    _check(lib().ifx_group_norm(d, x.data_ptr(), _addr(weight), _addr(bias), out.data_ptr(), mean.data_ptr(),
+                                rstd.data_ptr(), _addr(ws), nbytes, _raw_stream(stream, index)), "ifx_group_norm")
     return out, mean, rstd
 
 
@@ -647,18 +679,18 @@ def group_norm_mx4(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
                    out: Optional[Mx4] = None, stream=None) -> Mx4:
     """group_norm whose result is rounded to microscaled 4-bit codes instead of being stored, a row per
     pixel (ifx_group_norm_mx4)."""
-    device = _on_device(x, weight, bias, *(out[:2] if out is not None else ()))
+    index = _on_device(x, weight, bias, *(out[:2] if out is not None else ()))
     d = _gn_desc(x, groups, act, eps)
     _param(weight, d.c, "weight")
     _param(bias, d.c, "bias")
+    rows = d.n * d.hw
     if out is None:
-        out = mx4_empty(d.n * d.hw, d.c, device, stream)
-    _mx4_check(out, "out")
-    if (out.rows, out.k) != (d.n * d.hw, d.c):
-        raise ValueError(f"out of {out.rows} x {out.k}, x of {d.n * d.hw} pixels of {d.c} channels")
-    ws, nbytes = _gn_ws(d, 0, device, stream)
-    _check(lib().ifx_group_norm_mx4(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out.codes),
-                                    _ptr(out.scales), None, None, _ptr(ws), nbytes, _stream(stream)),
+        out = _mx4_like(rows, d.c, x, stream)
+    elif _mx4_check(out, "out") != rows or out.k != d.c:
+        raise ValueError(f"out of {out.rows} x {out.k}, x of {rows} pixels of {d.c} channels")
+    ws, nbytes = _gn_ws(d, 0, x, stream)
+    _check(lib().ifx_group_norm_mx4(d, x.data_ptr(), _addr(weight), _addr(bias), out.codes.data_ptr(),
+                                    out.scales.data_ptr(), None, None, _addr(ws), nbytes, _raw_stream(stream, index)),
            "ifx_group_norm_mx4")
     return out
 
@@ -668,22 +700,24 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                         act: int = ACT_NONE, out: Optional[torch.Tensor] = None, stream=None):
     """Gradient of group_norm (ifx_group_norm_backward) -> (dx, dweight [c], dbias [c]); mean and rstd are
     the forward pass's.  dweight and dbias are float32, also where weight or bias is None (1 and 0)."""
-    device = _on_device(dy, x, mean, rstd, weight, bias, out)
+    index = _on_device(dy, x, mean, rstd, weight, bias, out)
     d = _gn_desc(x, groups, act, 0.0)
     _param(weight, d.c, "weight")
     _param(bias, d.c, "bias")
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or tuple(t.shape) != (d.n, groups) or not t.is_contiguous():
+        if t.dtype != torch.float32 or t.shape != (d.n, groups) or not t.is_contiguous():
             raise ValueError(f"{name}: contiguous float32 of shape ({d.n}, {groups}) expected")
     d.ld_dy = _like(dy, x, "dy")
     if out is None:
-        out = _alloc(x.shape, x.dtype, device, stream)
-    d.ld_y = _like(out, x, "out")
-    dweight, dbias = (_alloc((d.c,), torch.float32, device, stream) for _ in range(2))
-    ws, nbytes = _gn_ws(d, 1, device, stream)
-    _check(lib().ifx_group_norm_backward(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                         _ptr(bias), _ptr(out), _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes,
-                                         _stream(stream)), "ifx_group_norm_backward")
+        out = _alloc(x.shape, x.dtype, x, stream)
+        d.ld_y = d.c
+    else:
+        d.ld_y = _like(out, x, "out")
+    dweight, dbias = _alloc((d.c,), torch.float32, x, stream), _alloc((d.c,), torch.float32, x, stream)
+    ws, nbytes = _gn_ws(d, 1, x, stream)
+    _check(lib().ifx_group_norm_backward(d, dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _addr(weight),
+                                         _addr(bias), out.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), _addr(ws),
+                                         nbytes, _raw_stream(stream, index)), "ifx_group_norm_backward")
     return out, dweight, dbias
 
 
