@@ -1308,7 +1308,7 @@ ifx_status check_gn_call(const ifx_gn_desc *d, bool backward, bool mx4, const vo
     if (!aligned_to(x, type_bytes(d->type)) || !aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(mean, 4) ||
         !aligned_to(rstd, 4) || !aligned16(ws))
         return IFX_E_ALIGN;
-    const size_t need = ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, backward);
+    const size_t need = ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, d->type, backward, mx4);
     if (need > ws_bytes) return IFX_E_WORKSPACE;
     return need > 0 && !ws ? IFX_E_NULL : IFX_OK;
 }
@@ -1402,7 +1402,9 @@ ifx_status ifx_mx4_matmul(const ifx_mx4_desc *d, const uint8_t *a_codes, const u
 size_t ifx_group_norm_workspace_bytes(const ifx_gn_desc *d, int32_t backward)
 {
     if (check_gn(d, backward != 0, false) != IFX_OK) return 0;
-    return ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, backward != 0);
+    const size_t need = ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, d->type, backward != 0, false);
+    if (backward) return need;
+    return std::max(need, ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, d->type, false, true));
 }
 
 ifx_status ifx_group_norm(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias, void *y,

@@ -170,6 +170,11 @@ struct GnArgs {
     int cg, cg_shr;
     unsigned cg_mul;
     int lpg, chunks, px;
+    // the resident form: groups of a span, spans of a sample, (sample, span) pairs of an XCD,
+    // division by cg / 8
+    int gs, spans, per_xcd;
+    unsigned cgv_mul;
+    int cgv_shr;
 };
 
 hipError_t launch_conv(const ConvArgs &a, int kh, int kw, hipStream_t s);
@@ -199,7 +204,7 @@ hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s);
 hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s);  // its tiled form, mx4_gemm.hip
 // group norm with an activation and its gradient, norm.hip
 bool gn_supported(int n, int hw, int c);
-size_t gn_workspace_bytes(int n, int hw, int c, int groups, bool grad);
+size_t gn_workspace_bytes(int n, int hw, int c, int groups, int type, bool grad, bool mx4);
 hipError_t launch_group_norm(GnArgs a, hipStream_t s);
 hipError_t launch_group_norm_grad(GnArgs a, float *dweight, float *dbias, hipStream_t s);
 hipError_t launch_fold_bn(const FoldArgs &f, int32_t *bias, int32_t *mult, int32_t *shift, int32_t *status,

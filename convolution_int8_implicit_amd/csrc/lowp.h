@@ -26,38 +26,93 @@ struct Elem<2> {
     typedef _Float16 type;
 };
 
-// Eight consecutive values as they lie in memory.  The struct carries the element's alignment
-// only, so one copy of it is a single 16-byte access (two for float) at any element boundary:
-// odd row pitches and slices need no path of their own.
+// Eight consecutive values as they lie in memory: four 32-bit words of a 16-bit type, eight of float.
+// Kept packed in registers and widened where they are used.
 template <typename E>
 struct Oct {
-    E v[8];
+    static constexpr int W = sizeof(E) * 2;
+    unsigned w[W];
+
+    __device__ __forceinline__ float get(int e) const
+    {
+        if constexpr (sizeof(E) == 4)
+            return __uint_as_float(w[e]);
+        else if constexpr (__is_same(E, __bf16))
+            return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        else
+            return (float)__builtin_bit_cast(_Float16, (unsigned short)(w[e / 2] >> (16 * (e & 1))));
+    }
+    // Makes the words opaque to the optimiser, which would otherwise keep the widened values of one
+    // use for the next, in twice the registers.
+    __device__ __forceinline__ void forget()
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
+    }
+};
+
+// Words aligned to the element only: one such access is a single 16-byte load or store at any
+// element boundary, so odd row pitches and slices need no path of their own.
+template <int ALIGN>
+struct Words;
+template <>
+struct Words<2> {
+    typedef unsigned type __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct Words<4> {
+    typedef unsigned type __attribute__((ext_vector_type(4), aligned(4)));
 };
 
 template <typename E>
-__device__ __forceinline__ void load8(const E *p, int valid, E (&raw)[8])
+__device__ __forceinline__ Oct<E> load8(const E *p, int valid)
 {
+    typedef typename Words<sizeof(E)>::type V;
+    Oct<E> o;
     if (valid >= 8) {
-        const Oct<E> o = *(const Oct<E> *)p;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) raw[e] = o.v[e];
+        for (int i = 0; i < Oct<E>::W / 4; ++i) {
+            const V v = ((const V *)p)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o.w[4 * i + j] = v[j];
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) raw[e] = e < valid ? p[e] : (E)0.0f;
+        for (int i = 0; i < Oct<E>::W; ++i) o.w[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < valid) {
+                if constexpr (sizeof(E) == 4)
+                    o.w[e] = ((const unsigned *)p)[e];
+                else
+                    o.w[e / 2] |= (unsigned)((const unsigned short *)p)[e] << (16 * (e & 1));
+            }
     }
+    return o;
+}
+
+template <typename E>
+__device__ __forceinline__ unsigned pack2(float a, float b)
+{
+    typedef E V __attribute__((ext_vector_type(2)));
+    const V v = {(E)a, (E)b};
+    return __builtin_bit_cast(unsigned, v);
 }
 
 template <typename E>
 __device__ __forceinline__ void store8(E *p, int valid, const float (&f)[8])
 {
+    typedef typename Words<sizeof(E)>::type V;
     if (valid >= 8) {
-        Oct<E> o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = (E)f[e];
-        *(Oct<E> *)p = o;
+        if constexpr (sizeof(E) == 4) {
+            ((V *)p)[0] = (V){__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+            ((V *)p)[1] = (V){__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
+        } else {
+            *(V *)p = (V){pack2<E>(f[0], f[1]), pack2<E>(f[2], f[3]), pack2<E>(f[4], f[5]), pack2<E>(f[6], f[7])};
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 7; ++e)
             if (e < valid) p[e] = (E)f[e];
     }
 }

@@ -39,18 +39,18 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *x, long l
     const int row = rt * kQRows + (t >> 4);
     const bool live = row < rows;
     const E *src = (const E *)x + (long long)(live ? row : rows - 1) * ld;
-    E raw[kQPanels][8];
+    Oct<E> raw[kQPanels];
 #pragma unroll
     for (int i = 0; i < kQPanels; ++i) {
         const int col = (pg * kQPanels + i) * 128 + v * 8;
-        load8(src + (col < k ? col : 0), k - col < 0 ? 0 : k - col, raw[i]);
+        raw[i] = load8(src + (col < k ? col : 0), k - col);
     }
 #pragma unroll
     for (int i = 0; i < kQPanels; ++i) {
         const int p = pg * kQPanels + i;
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (float)raw[i][e];
+        for (int e = 0; e < 8; ++e) f[e] = raw[i].get(e);
         unsigned s;
         const unsigned r = mx4_codes(f, s);
         if (live && p < k1) {
