@@ -24,7 +24,7 @@ LIB = os.path.join(LIBDIR, "libifx.so")
 ARCH = "gfx950"
 
 SOURCES = ["igemm.hip", "conv1x1.hip", "fold.hip", "stem.hip", "head.hip", "pack.hip", "probe.hip", "quant.hip",
-           "mx4.hip", "mx4_gemm.hip", "norm.hip", "api.cpp"]
+           "mx4.hip", "mx4_gemm.hip", "norm.hip", "norm_grad.hip", "api.cpp"]
 # gfx950 device code is built without packed-FP32 instructions; the host pass
 # warns that it does not know the feature, which is harmless.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -117,8 +117,12 @@ __device__ __forceinline__ void store8(E *p, int valid, const float (&f)[8])
     }
 }
 
-// Activations (include/ifx.h: IFX_ACT_NONE, IFX_ACT_RELU, IFX_ACT_SILU).  A NaN stays a NaN.
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// Activations (include/ifx.h: IFX_ACT_NONE, IFX_ACT_RELU, IFX_ACT_SILU).  A NaN stays a NaN.  The
+// sigmoid is one exponential and one reciprocal instruction, each good to a unit in the last place.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_of(float z)
@@ -127,9 +131,17 @@ __device__ __forceinline__ float act_of(float z)
     if (ACT == 2) return z * sigmoid(z);
     return z;
 }
-__device__ __forceinline__ float act_any(int act, float z)
+
+// f(tag) with the activation as a compile-time constant, so no value's loop chooses one.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f)
 {
-    return act == 1 ? act_of<1>(z) : act == 2 ? act_of<2>(z) : z;
+    if (act == 2)
+        f(Slot2());
+    else if (act == 1)
+        f(Slot1());
+    else
+        f(Slot0());
 }
 
 // Maximum over the four lanes 4i .. 4i + 3 (every lane of the wave active).

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_rows_kernel(Mx4Args a, int til
         if (m < a.m && n < a.n) {
             if (a.bias) f += a.bias[n];
             if (a.res) f += load_any(a.res, a.type, (long long)m * a.ld_res + n);
-            store_any(a.y, a.type, (long long)m * a.ld_y + n, act_any(a.act, f));
+            with_act(a.act, [&](auto act) { store_any(a.y, a.type, (long long)m * a.ld_y + n, act_of<decltype(act)::value>(f)); });
         }
     }
 }

@@ -195,46 +195,48 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     float bias[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) bias[e] = a.bias && e < left ? a.bias[col + e] : 0.0f;
+    with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-        const int r0 = m0 + wm * C::TM + i * 32;
-        if (r0 >= a.m) break;
+        for (int i = 0; i < C::FM; ++i) {
+            const int r0 = m0 + wm * C::TM + i * 32;
+            if (r0 >= a.m) break;
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
+            for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                *(float *)(out + (8 * (e / 4) + 4 * g + e % 4) * C::ROW + (j * 32 + c) * 4) = acc[i][j][e];
-        wave_lds_sync();
+                for (int e = 0; e < 16; ++e)
+                    *(float *)(out + (8 * (e / 4) + 4 * g + e % 4) * C::ROW + (j * 32 + c) * 4) = acc[i][j][e];
+            wave_lds_sync();
 #pragma unroll
-        for (int p = 0; p < 32 / RPP; ++p) {
-            const int r = p * RPP + l / LPR;
-            const long long row = r0 + r;
-            if (row >= a.m || left <= 0) continue;
-            const v4f f = *(const v4f *)(out + r * C::ROW + (l % LPR) * 16);
-            float v[4];
+            for (int p = 0; p < 32 / RPP; ++p) {
+                const int r = p * RPP + l / LPR;
+                const long long row = r0 + r;
+                if (row >= a.m || left <= 0) continue;
+                const v4f f = *(const v4f *)(out + r * C::ROW + (l % LPR) * 16);
+                float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = f[e] + bias[e];
-            if (left >= 4) {
-                if (a.res) {
-                    const Quad<E> q = *(const Quad<E> *)((const E *)a.res + row * a.ld_res + col);
+                for (int e = 0; e < 4; ++e) v[e] = f[e] + bias[e];
+                if (left >= 4) {
+                    if (a.res) {
+                        const Quad<E> q = *(const Quad<E> *)((const E *)a.res + row * a.ld_res + col);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += (float)q.v[e];
-                }
-                Quad<E> q;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) q.v[e] = (E)act_any(a.act, v[e]);
-                *(Quad<E> *)((E *)a.y + row * a.ld_y + col) = q;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < left) {
-                        if (a.res) v[e] += (float)((const E *)a.res)[row * a.ld_res + col + e];
-                        ((E *)a.y)[row * a.ld_y + col + e] = (E)act_any(a.act, v[e]);
+                        for (int e = 0; e < 4; ++e) v[e] += (float)q.v[e];
                     }
+                    Quad<E> q;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q.v[e] = (E)act_of<decltype(act)::value>(v[e]);
+                    *(Quad<E> *)((E *)a.y + row * a.ld_y + col) = q;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) {
+                            if (a.res) v[e] += (float)((const E *)a.res)[row * a.ld_res + col + e];
+                            ((E *)a.y)[row * a.ld_y + col + e] = (E)act_of<decltype(act)::value>(v[e]);
+                        }
+                }
             }
+            wave_lds_sync();
         }
-        wave_lds_sync();
-    }
+    });
 }
 
 typedef Tile<256, 256, 4, 2, 4> Tile256;
