@@ -45,13 +45,15 @@ struct Tile {
     static constexpr int STAGE = CODES + (BM + BN) * 4;
     static constexpr int CPW = (BM + BN) / 16 / W;  // 1 KB code DMAs per wave and stage
     static constexpr int SC = (BM + BN) / 64;       // 256-byte scale DMAs per stage
-    static constexpr int LPS = CPW + 1;             // DMAs per wave and stage
+    static constexpr int SPW = SC > W ? SC / W : 1; // of them per wave (waves past SC / SPW repeat others')
+    static constexpr int LPS = CPW + SPW;           // DMAs per wave and stage
     static constexpr int ROW = TN * 4 + 32;         // bytes of a staged output row: 4 rows apart, half the banks on
     static constexpr int OUT = 32 * ROW * W;
     static constexpr int LDS = ST * STAGE > OUT ? ST * STAGE : OUT;
     static constexpr int PER_CU = kLdsBytes / LDS < 2048 / T ? kLdsBytes / LDS : 2048 / T;
     static_assert(BM / 16 % CPW == 0, "a wave's code DMAs are all of A or all of W");
-    static_assert(SC <= W, "a wave brings one run of scales at most");
+    static_assert(SC <= W || SC % W == 0, "waves share the runs of scales evenly");
+    static_assert(BM / 64 % SPW == 0, "a wave's scale DMAs are all of A or all of W");
 };
 
 template <int N>
@@ -90,7 +92,7 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     const int row0 = of_a ? m0 : n0;
     const uint8_t *code_src = (of_a ? a.a_codes : a.w_codes) + (long long)row0 * 64;
     const long long code_range = min((long long)(of_a ? C::BM : C::BN), rows - row0) * 64;
-    const int sc = w % C::SC;
+    const int sc = w * C::SPW % C::SC;
     const bool s_of_a = sc < C::BM / 64;
     const long long s_rows = s_of_a ? a.m : a.n;
     const int s_row0 = s_of_a ? m0 : n0, s_chunk = s_of_a ? sc : sc - C::BM / 64;
@@ -100,13 +102,20 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     const unsigned scale_off = (unsigned)(s_chunk * 256 + l * 4);
     const int code_dst = w * C::CPW * 1024, scale_dst = C::CODES + sc * 256;
 
-    auto issue = [&](int s) __attribute__((always_inline)) {
+    // DMA j of this wave's LPS for step s
+    auto issue1 = [&](int s, int j) __attribute__((always_inline)) {
         int8_t *st = smem + (s % C::ST) * C::STAGE;
-        const v4i rc = make_rsrc(code_src + (long long)s * rows * 64, code_range);
+        if (j < C::CPW) {
+            load16_lds(make_rsrc(code_src + (long long)s * rows * 64, code_range), st + code_dst + j * 1024, code_off + j * 1024);
+        } else {
+            const int i = (j - C::CPW) * 256;
+            ifx_raw_buffer_load_lds(make_rsrc(scale_src + (long long)s * s_rows * 4, scale_range),
+                                    (__attribute__((address_space(3))) void *)(st + scale_dst + i), 4, scale_off + i, 0, 0, 0);
+        }
+    };
+    auto issue = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < C::CPW; ++j) load16_lds(rc, st + code_dst + j * 1024, code_off + j * 1024);
-        const v4i rs = make_rsrc(scale_src + (long long)s * s_rows * 4, scale_range);
-        ifx_raw_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)(st + scale_dst), 4, scale_off, 0, 0, 0);
+        for (int j = 0; j < C::LPS; ++j) issue1(s, j);
     };
 
     const int k1 = a.k1;
@@ -125,61 +134,74 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     const int a_sc = C::CODES + (wm * C::TM + c) * 4, b_sc = C::CODES + (C::BM + wn * C::TN + c) * 4;
     v4i a0[C::FM], b0[C::FN], a1[C::FM], b1[C::FN];
     int as[C::FM], bs[C::FN];
-    auto read0 = [&](const int8_t *st) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-            a0[i] = *(const v4i *)(st + a_row + q0 + i * 2048);
-            as[i] = *(const int *)(st + a_sc + i * 128);
-        }
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-            b0[j] = *(const v4i *)(st + b_row + q0 + j * 2048);
-            bs[j] = *(const int *)(st + b_sc + j * 128);
+    // fragment t of a step's first (HALF 0, with its rows' scales) or second half
+    constexpr int FR = C::FM + C::FN, MF = C::FM * C::FN;
+    constexpr int RD = (2 * FR + MF - 1) / MF;  // reads after a matrix instruction: all in the half's first half
+    auto read = [&](auto half, const int8_t *st, int t) __attribute__((always_inline)) {
+        constexpr int HALF = decltype(half)::value;
+        const int q = HALF ? q1 : q0;
+        const bool of = t < C::FM;
+        const int i = of ? t : t - C::FM;
+        const v4i v = *(const v4i *)(st + (of ? a_row : b_row) + q + i * 2048);
+        if (of)
+            (HALF ? a1 : a0)[i] = v;
+        else
+            (HALF ? b1 : b0)[i] = v;
+        if (!HALF) {
+            const int sc = *(const int *)(st + (of ? a_sc : b_sc) + i * 128);
+            if (of)
+                as[i] = sc;
+            else
+                bs[i] = sc;
         }
     };
 
     wait_later<C::LPS>(min(C::ST - 2, k1 - 1));
     ring_barrier();
-    read0(smem);
+#pragma unroll
+    for (int t = 0; t < FR; ++t) read(Slot0(), smem, t);
     int slot = 0;
-    // one step; `steady`: a further stage is requested and ST - 2 later ones stay in flight
+    // one step; `steady`: a further stage is requested and ST - 2 later ones stay in flight.  Reads and
+    // requests go out one by one between the matrix instructions: issued together they would hold up
+    // both waves of a SIMD at once.
     auto step = [&](auto steady, int s) __attribute__((always_inline)) {
         constexpr bool STEADY = decltype(steady)::value != 0;
         const int8_t *st = smem + slot * C::STAGE;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) a1[i] = *(const v4i *)(st + a_row + q1 + i * 2048);
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) b1[j] = *(const v4i *)(st + b_row + q1 + j * 2048);
-        if (STEADY) issue(s + C::ST - 1);
         int sa[C::FM], sb[C::FN];
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) sa[i] = (int)((unsigned)as[i] >> (8 * g));
+        for (int t = 0; t < MF; ++t) {
+            const int i = t / C::FN, j = t % C::FN;
+            if (j == 0) sa[i] = (int)((unsigned)as[i] >> (8 * g));
+            if (i == 0) sb[j] = (int)((unsigned)bs[j] >> (8 * g));
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(a0[i]), wide(b0[j]), acc[i][j], kFp4, kFp4, 0,
+                                                                        sa[i], 0, sb[j]);
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) sb[j] = (int)((unsigned)bs[j] >> (8 * g));
-        __builtin_amdgcn_sched_barrier(0);
+            for (int u = t * RD; u < (t + 1) * RD && u < FR; ++u) read(Slot1(), st, u);
+            if (STEADY)
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(a0[i]), wide(b0[j]), acc[i][j], kFp4, kFp4,
-                                                                            0, sa[i], 0, sb[j]);
-        __builtin_amdgcn_sched_barrier(0);
+                for (int u = t * C::LPS / MF; u < (t + 1) * C::LPS / MF; ++u) issue1(s + C::ST - 1, u);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         slot = slot + 1 == C::ST ? 0 : slot + 1;
-        if (STEADY || s + 1 < k1) {
+        const bool more = STEADY || s + 1 < k1;
+        if (more) {
             if (STEADY)
                 wait_vmcnt<(C::ST - 2) * C::LPS>();
             else
                 wait_later<C::LPS>(min(C::ST - 2, k1 - 2 - s));
             lds_barrier();  // the reads of stage s are complete, stage s + 1 has landed
-            read0(smem + slot * C::STAGE);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        const int8_t *next = smem + slot * C::STAGE;
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
+        for (int t = 0; t < MF; ++t) {
+            const int i = t / C::FN, j = t % C::FN;
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(a1[i]), wide(b1[j]), acc[i][j], kFp4, kFp4, 2,
+                                                                        sa[i], 2, sb[j]);
+            if (more)
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(a1[i]), wide(b1[j]), acc[i][j], kFp4, kFp4,
-                                                                            2, sa[i], 2, sb[j]);
+                for (int u = t * RD; u < (t + 1) * RD && u < FR; ++u) read(Slot0(), next, u);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     int s = 0;
     for (; s + C::ST - 1 < k1; ++s) step(Slot1(), s);
