@@ -30,6 +30,26 @@ constexpr int kFp4 = 4;  // the matrix instruction's operand format: 4-bit e2m1
 
 __device__ __forceinline__ v8i wide(v4i x) { return (v8i){x[0], x[1], x[2], x[3], 0, 0, 0, 0}; }
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// f(Int<0>()) .. f(Int<N - 1>())
+template <int I, int N, typename F>
+__device__ __forceinline__ void each_from(F &f)
+{
+    if constexpr (I < N) {
+        f(Int<I>());
+        each_from<I + 1, N>(f);
+    }
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(Int<N>, F f)
+{
+    each_from<0, N>(f);
+}
+
 // Four consecutive output values at any element boundary.
 template <typename E>
 struct Quad {
@@ -43,17 +63,16 @@ struct Tile {
     static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
     static constexpr int CODES = (BM + BN) * 64;
     static constexpr int STAGE = CODES + (BM + BN) * 4;
-    static constexpr int CPW = (BM + BN) / 16 / W;  // 1 KB code DMAs per wave and stage
-    static constexpr int SC = (BM + BN) / 64;       // 256-byte scale DMAs per stage
-    static constexpr int SPW = SC > W ? SC / W : 1; // of them per wave (waves past SC / SPW repeat others')
-    static constexpr int LPS = CPW + SPW;           // DMAs per wave and stage
+    static constexpr int CA = BM / 16 / W, CB = BN / 16 / W;  // 1 KB DMAs of A's and of W's codes per wave and stage
+    static constexpr int SC = (BM + BN) / 64;                 // 256-byte scale DMAs per stage
+    static constexpr int SPW = (SC + W - 1) / W;              // of them per wave (the last waves may repeat others')
+    static constexpr int LPS = CA + CB + SPW;                 // DMAs per wave and stage
     static constexpr int ROW = TN * 4 + 32;         // bytes of a staged output row: 4 rows apart, half the banks on
     static constexpr int OUT = 32 * ROW * W;
     static constexpr int LDS = ST * STAGE > OUT ? ST * STAGE : OUT;
     static constexpr int PER_CU = kLdsBytes / LDS < 2048 / T ? kLdsBytes / LDS : 2048 / T;
-    static_assert(BM / 16 % CPW == 0, "a wave's code DMAs are all of A or all of W");
-    static_assert(SC <= W || SC % W == 0, "waves share the runs of scales evenly");
-    static_assert(BM / 64 % SPW == 0, "a wave's scale DMAs are all of A or all of W");
+    static_assert(BM % (16 * W) == 0 && BN % (16 * W) == 0, "every wave brings as much of A and of W");
+    static_assert(SC % SPW == 0 && BM / 64 % SPW == 0, "a wave's scale DMAs are all of A or all of W");
 };
 
 template <int N>
@@ -85,38 +104,45 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     const int wm = w / C::WN, wn = w - wm * C::WN;
     const int c = l & 31, g = l >> 5;
 
-    // this wave's DMAs of a step: CPW kilobytes of A's or W's codes and 64 rows of scales
-    const bool of_a = w * C::CPW < C::BM / 16;
-    const int chunk0 = of_a ? w * C::CPW : w * C::CPW - C::BM / 16;
-    const long long rows = of_a ? a.m : a.n;
-    const int row0 = of_a ? m0 : n0;
-    const uint8_t *code_src = (of_a ? a.a_codes : a.w_codes) + (long long)row0 * 64;
-    const long long code_range = min((long long)(of_a ? C::BM : C::BN), rows - row0) * 64;
-    const int sc = w * C::SPW % C::SC;
-    const bool s_of_a = sc < C::BM / 64;
-    const long long s_rows = s_of_a ? a.m : a.n;
-    const int s_row0 = s_of_a ? m0 : n0, s_chunk = s_of_a ? sc : sc - C::BM / 64;
-    const uint8_t *scale_src = (s_of_a ? a.a_scales : a.w_scales) + (long long)s_row0 * 4;
-    const long long scale_range = min((long long)(s_of_a ? C::BM : C::BN), s_rows - s_row0) * 4;
-    const unsigned code_off = (unsigned)(chunk0 * 1024 + (l >> 2) * 64 + (((l & 3) ^ (l >> 4)) * 16));
-    const unsigned scale_off = (unsigned)(s_chunk * 256 + l * 4);
-    const int code_dst = w * C::CPW * 1024, scale_dst = C::CODES + sc * 256;
+    // this wave's DMAs of a step: CA and CB kilobytes of codes, SPW times 64 rows of scales.  Rows past a
+    // tensor's end lie past a resource's range and read as zeros.
+    const long long a_rows = min(C::BM, a.m - m0), w_rows = min(C::BN, a.n - n0);
+    const uint8_t *a_src = a.a_codes + (long long)m0 * 64, *w_src = a.w_codes + (long long)n0 * 64;
+    const long long a_step = (long long)a.m * 64, w_step = (long long)a.n * 64;
+    const int run = w * C::SPW % C::SC;
+    const bool s_of_a = run < C::BM / 64;
+    const uint8_t *s_src = s_of_a ? a.a_scales + (long long)m0 * 4 : a.w_scales + (long long)n0 * 4;
+    const long long s_step = (s_of_a ? a_step : w_step) / 16, s_rows = s_of_a ? a_rows : w_rows;
+    // One lane offset serves every code DMA: the wave's place goes into the resource's base, the DMA's into
+    // the instruction's offset, which counts in memory and in LDS alike.
+    const unsigned lane_off = (unsigned)((l >> 2) * 64 + (((l & 3) ^ (l >> 4)) * 16));
+    const unsigned scale_off = (unsigned)((s_of_a ? run : run - C::BM / 64) * 256 + l * 4);
+    static_assert(C::CA <= 4 && C::CB <= 4, "instruction offsets below 4096");
 
     // DMA j of this wave's LPS for step s
-    auto issue1 = [&](int s, int j) __attribute__((always_inline)) {
+    auto issue1 = [&](int s, auto jj) __attribute__((always_inline)) {
+        constexpr int j = decltype(jj)::value;
         int8_t *st = smem + (s % C::ST) * C::STAGE;
-        if (j < C::CPW) {
-            load16_lds(make_rsrc(code_src + (long long)s * rows * 64, code_range), st + code_dst + j * 1024, code_off + j * 1024);
+        typedef __attribute__((address_space(3))) void *Lds;
+        if constexpr (j < C::CA) {
+            const int at = w * C::CA * 1024;
+            ifx_raw_buffer_load_lds(make_rsrc(a_src + s * a_step + at, a_rows * 64 - at), (Lds)(st + at), 16, lane_off, 0,
+                                    j * 1024, 0);
+        } else if constexpr (j < C::CA + C::CB) {
+            const int at = w * C::CB * 1024;
+            ifx_raw_buffer_load_lds(make_rsrc(w_src + s * w_step + at, w_rows * 64 - at), (Lds)(st + C::BM * 64 + at), 16,
+                                    lane_off, 0, (j - C::CA) * 1024, 0);
         } else {
-            const int i = (j - C::CPW) * 256;
-            ifx_raw_buffer_load_lds(make_rsrc(scale_src + (long long)s * s_rows * 4, scale_range),
-                                    (__attribute__((address_space(3))) void *)(st + scale_dst + i), 4, scale_off + i, 0, 0, 0);
+            constexpr int i = (j - C::CA - C::CB) * 256;
+            ifx_raw_buffer_load_lds(make_rsrc(s_src + s * s_step, s_rows * 4), (Lds)(st + C::CODES + run * 256), 4, scale_off,
+                                    0, i, 0);
         }
     };
-    auto issue = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < C::LPS; ++j) issue1(s, j);
+    auto issue_some = [&](int s, auto after, auto upto) __attribute__((always_inline)) {
+        auto one = [&](auto j) __attribute__((always_inline)) { issue1(s, j); };
+        each_from<decltype(after)::value, decltype(upto)::value>(one);
     };
+    auto issue = [&](int s) __attribute__((always_inline)) { issue_some(s, Int<0>(), Int<C::LPS>()); };
 
     const int k1 = a.k1;
 #pragma unroll
@@ -168,20 +194,17 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
         constexpr bool STEADY = decltype(steady)::value != 0;
         const int8_t *st = smem + slot * C::STAGE;
         int sa[C::FM], sb[C::FN];
-#pragma unroll
-        for (int t = 0; t < MF; ++t) {
-            const int i = t / C::FN, j = t % C::FN;
+        each(Int<MF>(), [&](auto tt) __attribute__((always_inline)) {
+            constexpr int t = decltype(tt)::value, i = t / C::FN, j = t % C::FN;
             if (j == 0) sa[i] = (int)((unsigned)as[i] >> (8 * g));
             if (i == 0) sb[j] = (int)((unsigned)bs[j] >> (8 * g));
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(a0[i]), wide(b0[j]), acc[i][j], kFp4, kFp4, 0,
                                                                         sa[i], 0, sb[j]);
 #pragma unroll
             for (int u = t * RD; u < (t + 1) * RD && u < FR; ++u) read(Slot1(), st, u);
-            if (STEADY)
-#pragma unroll
-                for (int u = t * C::LPS / MF; u < (t + 1) * C::LPS / MF; ++u) issue1(s + C::ST - 1, u);
+            if (STEADY) issue_some(s + C::ST - 1, Int<t * C::LPS / MF>(), Int<(t + 1) * C::LPS / MF>());
             __builtin_amdgcn_sched_barrier(0);
-        }
+        });
         slot = slot + 1 == C::ST ? 0 : slot + 1;
         const bool more = STEADY || s + 1 < k1;
         if (more) {
@@ -209,61 +232,70 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
 
     // Epilogue, 32 rows of the wave's tile at a time: the accumulators (lane l: column l % 32, rows
     // 8 (i / 4) + 4 (l / 32) + i % 4) go through LDS into rows, so bias, residual and output move four
-    // columns a lane in whole rows.
+    // columns a lane in whole rows.  The rows' residual is requested before they are staged.
     lds_barrier();
+    // the lane anew: values kept from before the loop would cost registers in it
+    int el = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    asm volatile("" : "+v"(el));
     int8_t *out = smem + w * 32 * C::ROW;
-    constexpr int LPR = C::TN / 4, RPP = 64 / LPR;  // lanes per row, rows per pass
-    const int col = n0 + wn * C::TN + (l % LPR) * 4, left = a.n - col;
+    constexpr int LPR = C::TN / 4, RPP = 64 / LPR, P = 32 / RPP;  // lanes per row, rows per pass, passes
+    const int col = n0 + wn * C::TN + (el % LPR) * 4, left = a.n - col;
+    const bool whole = left >= 4;  // all of the lane's columns exist
     float bias[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bias[e] = a.bias && e < left ? a.bias[col + e] : 0.0f;
-    with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+    for (int e = 0; e < 4; ++e) bias[e] = a.bias && whole ? a.bias[col + e] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-            const int r0 = m0 + wm * C::TM + i * 32;
-            if (r0 >= a.m) break;
+    for (int i = 0; i < C::FM; ++i) {
+        const int r0 = m0 + wm * C::TM + i * 32;
+        if (r0 >= a.m) break;
+        const long long row0 = r0 + el / LPR;
+        Quad<E> res[P];
+        if (a.res) {
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j)
+            for (int p = 0; p < P; ++p)
+                if (whole && row0 + p * RPP < a.m) res[p] = *(const Quad<E> *)((const E *)a.res + (row0 + p * RPP) * a.ld_res + col);
+        }
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    *(float *)(out + (8 * (e / 4) + 4 * g + e % 4) * C::ROW + (j * 32 + c) * 4) = acc[i][j][e];
-            wave_lds_sync();
+        for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-            for (int p = 0; p < 32 / RPP; ++p) {
-                const int r = p * RPP + l / LPR;
-                const long long row = r0 + r;
-                if (row >= a.m || left <= 0) continue;
-                const v4f f = *(const v4f *)(out + r * C::ROW + (l % LPR) * 16);
-                float v[4];
+            for (int e = 0; e < 16; ++e)
+                *(float *)(out + (8 * (e / 4) + 4 * (el >> 5) + e % 4) * C::ROW + (j * 32 + (el & 31)) * 4) = acc[i][j][e];
+        wave_lds_sync();
+        with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act)::value;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = f[e] + bias[e];
-                if (left >= 4) {
-                    if (a.res) {
-                        const Quad<E> q = *(const Quad<E> *)((const E *)a.res + row * a.ld_res + col);
+            for (int p = 0; p < P; ++p) {
+                const v4f f = *(const v4f *)(out + (p * RPP + el / LPR) * C::ROW + (el % LPR) * 16);
+                Quad<E> q;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] += (float)q.v[e];
-                    }
-                    Quad<E> q;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) q.v[e] = (E)act_of<decltype(act)::value>(v[e]);
-                    *(Quad<E> *)((E *)a.y + row * a.ld_y + col) = q;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < left) {
-                            if (a.res) v[e] += (float)((const E *)a.res)[row * a.ld_res + col + e];
-                            ((E *)a.y)[row * a.ld_y + col + e] = (E)act_of<decltype(act)::value>(v[e]);
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    float v = f[e] + bias[e];
+                    if (a.res) v += (float)res[p].v[e];
+                    q.v[e] = (E)act_of<ACT>(v);
+                }
+                if (whole && row0 + p * RPP < a.m) *(Quad<E> *)((E *)a.y + (row0 + p * RPP) * a.ld_y + col) = q;
+            }
+            if (left > 0 && !whole) {  // the last one to three columns of y, value by value
+#pragma unroll 1
+                for (int k = 0; k < P * left; ++k) {
+                    const int p = k / left, e = k - p * left;
+                    const long long row = row0 + p * RPP;
+                    if (row >= a.m) break;
+                    float v = *(const float *)(out + (p * RPP + el / LPR) * C::ROW + (el % LPR) * 16 + e * 4);
+                    if (a.bias) v += a.bias[col + e];
+                    if (a.res) v += (float)((const E *)a.res)[row * a.ld_res + col + e];
+                    ((E *)a.y)[row * a.ld_y + col + e] = (E)act_of<ACT>(v);
                 }
             }
-            wave_lds_sync();
-        }
-    });
+        });
+        wave_lds_sync();
+    }
 }
 
-typedef Tile<256, 256, 4, 2, 4> Tile256;
-typedef Tile<128, 128, 2, 2, 4> Tile128;
-typedef Tile<64, 64, 2, 2, 4> Tile64;
+// Three tiles, two of the larger ones' workgroups on a CU (one's epilogue behind the other's steps).
+typedef Tile<256, 128, 4, 2, 3> TileL;
+typedef Tile<128, 128, 4, 2, 3> TileM;
+typedef Tile<64, 64, 2, 2, 4> TileS;
 
 template <typename C>
 hipError_t launch(const Mx4Args &a, hipStream_t s)
@@ -275,7 +307,11 @@ hipError_t launch(const Mx4Args &a, hipStream_t s)
     return hipGetLastError();
 }
 
-long long tiles(const Mx4Args &a, int size) { return ((a.m - 1LL) / size + 1) * ((a.n - 1LL) / size + 1); }
+template <typename C>
+long long tiles(const Mx4Args &a)
+{
+    return ((a.m - 1LL) / C::BM + 1) * ((a.n - 1LL) / C::BN + 1);
+}
 
 }  // namespace
 
@@ -283,9 +319,14 @@ hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s)
 {
     int cus = 0;
     if (current_cus(&cus) != hipSuccess) cus = 256;
-    if (tiles(a, 256) >= cus) return launch<Tile256>(a, s);
-    if (tiles(a, 128) >= cus) return launch<Tile128>(a, s);
-    return launch<Tile64>(a, s);
+    // The largest tile that gives every CU one (256 CUs; us, large / middle / small tile):
+    //   8192 x 2048 x 256 (512 large tiles)    12.4 / 14.4 / 16.8
+    //   4096 x 2048 x 2048 (256 large)         17.4 / 18.1 / 21.6
+    //   2048 x 2048 x 2048 (256 middle)        13.7 / 11.1 / 12.8
+    //   1024 x 2048 x 2048 (128 middle)        12.5 /  9.9 /  8.5
+    if (tiles<TileL>(a) >= cus) return launch<TileL>(a, s);
+    if (tiles<TileM>(a) >= cus) return launch<TileM>(a, s);
+    return launch<TileS>(a, s);
 }
 
 }  // namespace ifx
