@@ -112,36 +112,63 @@ __device__ __forceinline__ void store_any(void *p, int type, long long i, float 
         ((_Float16 *)p)[i] = (_Float16)f;
 }
 
-// Few rows: a workgroup of WAVES waves takes 16 weight rows and 16 rows of A; wave w multiplies
-// panels w, w + WAVES, ... straight from memory (16 rows of a panel are one contiguous kilobyte,
-// one 16-byte load per lane) and the partial sums meet in LDS, summed in wave order.
+// Few rows: a workgroup of kRowWaves waves takes 16 weight rows and 16 MT rows of A; wave w multiplies
+// panels w, w + kRowWaves, ... straight from memory (16 rows of a panel are one contiguous kilobyte,
+// one 16-byte load per lane), kAhead of them requested at once, and the partial sums meet in LDS,
+// added in wave order.  What bounds it: the weights, read once for MT = 1.
 // The 16x16x128 instruction takes row l % 16 and columns 32 (l / 16) .. + 31 from lane l, one
 // block with its scale in the lowest byte; lane l's results are column l % 16 (a row of A here)
 // and rows 4 (l / 16) .. + 3 (weight rows).
-template <int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void mx4_rows_kernel(Mx4Args a, int tiles_n)
+// 8 waves and 4 panels ahead measured best (one row of 8192 x 8192 from HBM 9.8 us, launch included, 3.6 TB/s;
+// 16 waves 11.5, 8 panels ahead 11.8, 2 panels 10.0, 4 waves 9.9).
+constexpr int kRowWaves = 8, kAhead = 4;
+
+template <int MT>
+__global__ __launch_bounds__(64 * kRowWaves) void mx4_rows_kernel(Mx4Args a, int tiles_n)
 {
-    __shared__ float part[WAVES][256];
+    __shared__ float part[kRowWaves][MT * 256];
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63, c = l & 15, g = l >> 4;
     const unsigned tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x - tm * (unsigned)tiles_n;
-    const int m0 = (int)tm * 16, n0 = (int)tn * 16;
-    const int ar = min(m0 + c, a.m - 1), wr = min(n0 + c, a.n - 1);
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p = w; p < a.k1; p += WAVES) {
-        const long long ai = (long long)p * a.m + ar, wi = (long long)p * a.n + wr;
-        const v4i av = ((const v4i *)a.a_codes)[ai * 4 + g];
-        const v4i wv = ((const v4i *)a.w_codes)[wi * 4 + g];
-        const int as = a.a_scales[ai * 4 + g], ws = a.w_scales[wi * 4 + g];
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(wv), wide(av), acc, kFp4, kFp4, 0, ws, 0, as);
+    const int m0 = (int)tm * 16 * MT, n0 = (int)tn * 16;
+    const int wr = min(n0 + c, a.n - 1);
+    v4f acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p0 = w; p0 < a.k1; p0 += kAhead * kRowWaves) {
+        v4i wv[kAhead], av[kAhead][MT];
+        int ws[kAhead], as[kAhead][MT];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const long long p = p0 + u * kRowWaves;
+            if (p < a.k1) {
+                const long long wi = (p * a.n + wr) * 4 + g;
+                wv[u] = ((const v4i *)a.w_codes)[wi];
+                ws[u] = a.w_scales[wi];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const long long ai = (p * a.m + min(m0 + 16 * t + c, a.m - 1)) * 4 + g;
+                    av[u][t] = ((const v4i *)a.a_codes)[ai];
+                    as[u][t] = a.a_scales[ai];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (p0 + u * kRowWaves < a.k1)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(wv[u]), wide(av[u][t]), acc[t], kFp4, kFp4,
+                                                                             0, ws[u], 0, as[u][t]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[w][c * 16 + 4 * g + i] = acc[i];
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[w][t * 256 + c * 16 + 4 * g + i] = acc[t][i];
     __syncthreads();
-    const int t = threadIdx.x;
-    if (t < 256) {
+    for (int t = threadIdx.x; t < MT * 256; t += 64 * kRowWaves) {
         float f = 0.0f;
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) f += part[i][t];
+        for (int i = 0; i < kRowWaves; ++i) f += part[i][t];
         const int m = m0 + (t >> 4), n = n0 + (t & 15);
         if (m < a.m && n < a.n) {
             if (a.bias) f += a.bias[n];
@@ -149,6 +176,14 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_rows_kernel(Mx4Args a, int til
             with_act(a.act, [&](auto act) { store_any(a.y, a.type, (long long)m * a.ld_y + n, act_of<decltype(act)::value>(f)); });
         }
     }
+}
+
+template <int MT>
+void launch_rows(const Mx4Args &a, hipStream_t s)
+{
+    const int tiles_n = (a.n - 1) / 16 + 1;
+    const dim3 grid((unsigned)(((a.m - 1) / (16 * MT) + 1) * tiles_n));
+    hipLaunchKernelGGL(mx4_rows_kernel<MT>, grid, dim3(64 * kRowWaves), 0, s, a, tiles_n);
 }
 
 }  // namespace
@@ -175,10 +210,18 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
 
 hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s)
 {
-    if (a.m > 64) return launch_mx4_tiles(a, s);
-    const int tiles_n = (a.n + 15) / 16;
-    const dim3 grid((unsigned)((a.m + 15LL) / 16 * tiles_n));
-    hipLaunchKernelGGL(mx4_rows_kernel<8>, grid, dim3(512), 0, s, a, tiles_n);
+    // The few-rows form reads the weights once a group of 64 rows, a tile of 64 rows costs the same from
+    // 1 row to 64 (us, few rows / tiles, weights from HBM): 1 x 8192 x 8192 9.8 / 17.9, 32 rows 13.9 / 18.0,
+    // 64 rows 21.9 / 18.2; 64 x 4096 x 4096, one workgroup a CU, 7.2 / 8.8; 64 x 1000 x 2048 5.0 / 5.8.
+    int cus = 0;
+    if (current_cus(&cus) != hipSuccess) cus = 256;
+    if (a.m > 64 || (a.m > 32 && a.n > 16 * cus)) return launch_mx4_tiles(a, s);
+    if (a.m <= 16)
+        launch_rows<1>(a, s);
+    else if (a.m <= 32)
+        launch_rows<2>(a, s);
+    else
+        launch_rows<4>(a, s);
     return hipGetLastError();
 }
 
