@@ -1294,7 +1294,7 @@ ifx_status check_gn(const ifx_gn_desc *d, bool backward, bool mx4)
     if (!pitch_ok(rows, d->c, d->ld_x) || (!mx4 && !pitch_ok(rows, d->c, d->ld_y))) return IFX_E_SHAPE;
     if (backward && !pitch_ok(rows, d->c, d->ld_dy)) return IFX_E_SHAPE;
     if (d->hw > 0x3fffffff || (mx4 && rows > 0x7fffffffLL)) return IFX_E_SHAPE;
-    return ifx::gn_supported(d->n, d->hw, d->c) ? IFX_OK : IFX_E_UNSUPPORTED;
+    return ifx::gn_supported(d->n, d->hw, d->c, d->groups) ? IFX_OK : IFX_E_UNSUPPORTED;
 }
 
 // What the three group norm calls share: the descriptor, x, the parameters, mean and rstd, the workspace.

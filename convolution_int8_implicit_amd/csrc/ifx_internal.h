@@ -203,7 +203,7 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
 hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s);
 hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s);  // its tiled form, mx4_gemm.hip
 // group norm with an activation and its gradient, norm.hip
-bool gn_supported(int n, int hw, int c);
+bool gn_supported(int n, int hw, int c, int groups);
 size_t gn_workspace_bytes(int n, int hw, int c, int groups, int type, bool grad, bool mx4);
 hipError_t launch_group_norm(GnArgs a, hipStream_t s);
 hipError_t launch_group_norm_grad(GnArgs a, float *dweight, float *dbias, hipStream_t s);

@@ -223,7 +223,8 @@ __global__ __launch_bounds__(T) void gn_stats_kernel(GnArgs a)
     for (int i = threadIdx.x; i < a.groups; i += T) out[2 * i + 1] = gs[i];
 }
 
-// Joins the chunks' statistics of sample n: smean[g], srstd[g].
+// Joins the chunks' statistics of sample n: smean[g], srstd[g].  A lane has all of its chunks' parts in
+// flight at once.
 template <int T>
 __device__ __forceinline__ void join_stats(const GnArgs &a, int n, float *smean, float *srstd)
 {
@@ -234,16 +235,25 @@ __device__ __forceinline__ void join_stats(const GnArgs &a, int n, float *smean,
     const float full = (float)a.px * (float)a.cg, rest = (float)(a.hw - (a.chunks - 1) * a.px) * (float)a.cg;
     const int sub = (int)threadIdx.x & (a.lpg - 1);
     for (int g = (int)threadIdx.x / a.lpg; g < a.groups; g += T / a.lpg) {
+        v2f t[kJoin];
         float f = 0.0f;
-#pragma unroll 8
-        for (int k = sub; k < a.chunks; k += a.lpg) f = fmaf(ws[k * a.groups + g].x, k == a.chunks - 1 ? rest : full, f);
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            const int k = sub + i * a.lpg;
+            t[i] = k < a.chunks ? ws[k * a.groups + g] : (v2f){0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            const int k = sub + i * a.lpg;
+            f = fmaf(t[i].x, k < a.chunks - 1 ? full : k == a.chunks - 1 ? rest : 0.0f, f);
+        }
         const float mean = lanes_sum(f, a.lpg) / total;
         f = 0.0f;
-#pragma unroll 8
-        for (int k = sub; k < a.chunks; k += a.lpg) {
-            const v2f t = ws[k * a.groups + g];
-            const float d = t.x - mean;
-            f += fmaf(d * d, k == a.chunks - 1 ? rest : full, t.y);
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            const int k = sub + i * a.lpg;
+            const float d = t[i].x - mean;
+            f += fmaf(d * d, k < a.chunks - 1 ? full : k == a.chunks - 1 ? rest : 0.0f, t[i].y);
         }
         const float var = lanes_sum(f, a.lpg) / total;
         if (sub == 0) {
@@ -255,49 +265,54 @@ __device__ __forceinline__ void join_stats(const GnArgs &a, int n, float *smean,
 }
 
 // The chunks joined, then each pixel normalised.  MX4: threads also cover the columns up to the next
-// multiple of 128.
+// multiple of 128.  The first pixels and the parameters are requested before the join.
 template <int T, int TYPE, bool MX4>
 __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
     __shared__ float smean[T * 8], srstd[T * 8];
+    constexpr int AHEAD = 4;  // loads in flight
     const Chunk s = chunk_of(a);
-    join_stats<T>(a, s.n, smean, srstd);
-    if (s.k == 0)
-        for (int i = threadIdx.x; i < a.groups; i += T) {
-            if (a.mean) a.mean[(long long)s.n * a.groups + i] = smean[i];
-            if (a.rstd) a.rstd[(long long)s.n * a.groups + i] = srstd[i];
-        }
     const Place p = place<T>(MX4 ? (a.c + 127) / 128 * 16 : (a.c + 7) / 8);
-    if (!p.active) return;
     const int valid = a.c - p.vec * 8;
+    const long long first = (long long)s.n * a.hw;
+    const Pixels<E> x(a.x, a, a.ld_x);
+    Oct<E> raw[AHEAD];
+    auto request = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (q + i * p.tp < s.p1 && p.active && valid > 0)
+                raw[i] = x.get(first + q + i * p.tp, p.vec * 8, valid);
+            else
+                raw[i] = {};
+    };
+    if (T == 1024) join_stats<T>(a, s.n, smean, srstd);  // first here: 128 registers do not hold both
+    request(s.p0 + p.pl);
     Affine<TYPE, false> f;
-    PerGroup<false> m, r;
-    m.set(p, s, a, [&](int g) { return smean[g]; });
-    r.set(p, s, a, [&](int g) { return srstd[g]; });
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int ch = p.vec * 8 + e;
         f.w[e] = e >= valid ? 0.0f : a.weight ? a.weight[ch] : 1.0f;
         f.b[e] = e >= valid || !a.bias ? 0.0f : a.bias[ch];
     }
+    if (T != 1024) join_stats<T>(a, s.n, smean, srstd);
+    if (s.k == 0)
+        for (int i = threadIdx.x; i < a.groups; i += T) {
+            if (a.mean) a.mean[(long long)s.n * a.groups + i] = smean[i];
+            if (a.rstd) a.rstd[(long long)s.n * a.groups + i] = srstd[i];
+        }
+    if (!p.active) return;
+    PerGroup<false> m, r;
+    m.set(p, s, a, [&](int g) { return smean[g]; });
+    r.set(p, s, a, [&](int g) { return srstd[g]; });
     f.set(m, r);
-    const long long first = (long long)s.n * a.hw;
-    const Pixels<E> x(a.x, a, a.ld_x);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
-        constexpr int AHEAD = 4;  // loads in flight
         for (int q = s.p0 + p.pl; q < s.p1; q += AHEAD * p.tp) {
-            Oct<E> raw[AHEAD];
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (q + i * p.tp < s.p1 && valid > 0)
-                    raw[i] = x.get(first + q + i * p.tp, p.vec * 8, valid);
-                else
-                    raw[i] = {};
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
                 if (q + i * p.tp < s.p1)
                     put_pixel<decltype(act)::value, TYPE, MX4, false>(raw[i], f, first + q + i * p.tp, p.vec * 8, valid, a);
+            request(q + AHEAD * p.tp);
         }
     });
 }
@@ -306,17 +321,26 @@ __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
 // Host side
 // ------------------------------------------------------------------------------------------
 
-// A chunk gives every thread at least one batch, and there are about 1024 workgroups where the work
-// allows it.
-Plan plan_split(int n, int hw, int c)
+// Lanes that sum one group where `groups` groups are summed at once.
+int sum_lanes(int groups, int threads)
+{
+    int lanes = 1;
+    while (lanes < 64 && lanes * 2 * groups <= threads) lanes *= 2;
+    return lanes;
+}
+
+// A chunk gives every thread at least one batch, a lane of the join has at most kJoin chunks, and there are
+// about 1024 workgroups where the work allows it.
+Plan plan_split(int n, int hw, int c, int groups)
 {
     Plan p = {};
-    p.threads = c <= 2048 ? 256 : 1024;
+    p.threads = c <= 2048 ? 512 : 1024;
     const int tp = p.threads / ((c + 7) / 8);
     const int most = (hw + kBatch * tp - 1) / (kBatch * tp);
     const int want = n > 0 ? (1024 + n - 1) / n : 1;
     int chunks = want < most ? want : most;
-    if (chunks > 256) chunks = 256;
+    const int limit = kJoin * sum_lanes(groups, p.threads);
+    if (chunks > limit) chunks = limit;
     if (chunks < 1) chunks = 1;
     p.px = (hw + chunks - 1) / chunks;
     p.chunks = (hw + p.px - 1) / p.px;
@@ -352,35 +376,41 @@ GnKernel slab_kernel_of(const Plan &p, int type)
 
 }  // namespace
 
-// Slab where a span of whole groups that reads at least 128 (else 64, else 32) bytes of a pixel fits the
-// registers of a workgroup.  A 4-bit result needs spans of whole blocks of 32 columns.
+// Slab where a span of whole groups fits the registers of a workgroup.  The span reads at least 128 bytes of
+// a pixel; at least 64 where that makes a slab of more than 32768 values (us, bf16, 128 / 64 bytes: 64 x 784
+// x 512 24.8 / 23.7, its gradient 53 / 45, but 256 x 196 x 1024 41 / 48) or does not fit; and down to 16 where
+// the spans are too few to give every CU one (1 x 3136 x 256: 16.7 at 64 bytes, 8.6 at 16; the
+// neighbouring spans of so small a tensor meet in the caches) or 64 does not fit.  A 4-bit result
+// needs spans of whole blocks of 32 columns.
 Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
 {
     const int cg = c / groups, bytes = type == 0 ? 4 : 2;
+    int cus = 0;
+    if (current_cus(&cus) != hipSuccess) cus = 256;
     // registers for raw values: 64 of a thread's 128, half where a channel's group takes registers of its own
     int most = (type == 0 ? 8 : 16) / (grad ? 2 : 1);
     if (cg % 8 && (type != 0 || grad)) most /= 2;
-    for (int least = 128; least >= 32; least /= 2)
-        for (int gs = 1; gs <= groups; ++gs) {
-            if (groups % gs) continue;
-            const int cs = gs * cg;
-            if (cs * bytes < least && gs < groups) continue;
-            if (mx4 && cs % 32 && gs < groups) continue;
-            // a last span of 4-bit codes is padded to whole panels
-            const int tcv = (cs + 7) / 8 + (mx4 ? (c + 127) / 128 * 16 - (c + 7) / 8 : 0);
-            for (const Variant &v : grad ? kGradSlab : kSlab) {
-                if (v.nv > most || tcv > v.threads / 4 || (long long)v.threads / tcv * v.nv < hw) continue;
-                if (n > 0 && (long long)n * (groups / gs) * v.threads > 0x7fffffffLL) continue;
-                Plan p = {};
-                p.threads = v.threads;
-                p.nv = v.nv;
-                p.gs = gs;
-                p.spans = groups / gs;
-                return p;
+    Plan best = {};
+    for (int least = 128; least >= 16; least /= 2) {
+        int gs = 1;
+        while (gs < groups && (groups % gs || gs * cg * bytes < least || (mx4 && gs * cg % 32))) ++gs;
+        const int cs = gs * cg;
+        // a last span of 4-bit codes is padded to whole panels
+        const int tcv = (cs + 7) / 8 + (mx4 ? (c + 127) / 128 * 16 - (c + 7) / 8 : 0);
+        if ((long long)n * (groups / gs) > (1 << 20)) break;  // the grid
+        const bool enough = n == 0 || (long long)n * (groups / gs) >= cus;
+        if (best.nv && ((least < 64 && best.spans * (long long)n >= cus) || best.gs == gs)) break;
+        for (const Variant &v : grad ? kGradSlab : kSlab)
+            if (v.nv <= most && tcv <= v.threads / 4 && (long long)v.threads / tcv * v.nv >= hw) {
+                best.threads = v.threads;
+                best.nv = v.nv;
+                best.gs = gs;
+                best.spans = groups / gs;
+                break;
             }
-            break;  // a wider span fits no better
-        }
-    return plan_split(n, hw, c);
+        if (best.nv && enough && (long long)hw * cs <= 32768) break;
+    }
+    return best.nv ? best : plan_split(n, hw, c, groups);
 }
 
 void gn_fill(GnArgs &a, const Plan &p)
@@ -393,9 +423,7 @@ void gn_fill(GnArgs &a, const Plan &p)
     a.gs = p.gs;
     a.spans = p.spans;
     a.per_xcd = (int)(((long long)a.n * p.spans + 7) / 8);
-    const int sums = p.nv ? p.gs : a.groups;
-    a.lpg = 1;
-    while (a.lpg < 64 && a.lpg * 2 * sums <= p.threads) a.lpg *= 2;
+    a.lpg = sum_lanes(p.nv ? p.gs : a.groups, p.threads);
 }
 
 size_t gn_workspace_bytes(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
@@ -406,10 +434,10 @@ size_t gn_workspace_bytes(int n, int hw, int c, int groups, int type, bool grad,
     return rows * 4 * 2 * ((size_t)groups + (grad ? (size_t)c : 0));
 }
 
-bool gn_supported(int n, int hw, int c)
+bool gn_supported(int n, int hw, int c, int groups)
 {
     if (c > kMaxC) return false;
-    const Plan p = plan_split(n, hw, c);
+    const Plan p = plan_split(n, hw, c, groups);
     return (long long)n * p.chunks * p.threads <= 0xffffffffLL;
 }
 
@@ -428,9 +456,9 @@ hipError_t launch_group_norm(GnArgs a, hipStream_t s)
     }
     const dim3 grid((unsigned)(a.n * p.chunks));
     GnKernel stats, apply;
-    if (p.threads == 256) {
-        stats = vec ? IFX_GN_TYPES(gn_stats_kernel, 256, true) : IFX_GN_TYPES(gn_stats_kernel, 256, false);
-        apply = mx4 ? IFX_GN_TYPES(gn_apply_kernel, 256, true) : IFX_GN_TYPES(gn_apply_kernel, 256, false);
+    if (p.threads == 512) {
+        stats = vec ? IFX_GN_TYPES(gn_stats_kernel, 512, true) : IFX_GN_TYPES(gn_stats_kernel, 512, false);
+        apply = mx4 ? IFX_GN_TYPES(gn_apply_kernel, 512, true) : IFX_GN_TYPES(gn_apply_kernel, 512, false);
     } else {
         stats = vec ? IFX_GN_TYPES(gn_stats_kernel, 1024, true) : IFX_GN_TYPES(gn_stats_kernel, 1024, false);
         apply = mx4 ? IFX_GN_TYPES(gn_apply_kernel, 1024, true) : IFX_GN_TYPES(gn_apply_kernel, 1024, false);

@@ -24,6 +24,7 @@ namespace ifx {
 
 constexpr int kMaxC = 8192;  // channels: eight per thread, 1024 threads
 constexpr int kBatch = 8;    // pixels a thread of the split form holds at once
+constexpr int kJoin = 16;    // chunks' parts that a lane joins at most
 
 // ------------------------------------------------------------------------------------------
 // Device side

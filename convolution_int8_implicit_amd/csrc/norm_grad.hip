@@ -3,27 +3,48 @@
 // One sum over the pixels serves everything: with S1[ch] = sum dz xhat and S2[ch] = sum dz, dweight and
 // dbias are their sums over the samples, and a group's sums of d xhat and d are those of weight S1 and
 // weight S2 over its channels.  What bounds it: three passes of memory (x, dy, dx) in the slab form,
-// and the vector units (about 45 operations a value with SiLU).
+// and the vector units (about 40 operations a value with SiLU).
 #include "norm_common.h"
 
 namespace ifx {
 namespace {
 
-// dz and xhat of one value.  z takes the operations of its formula one at a time, unfused, so that the
-// side of a ReLU's corner on which a value lies is the formula's own.
-template <int ACT>
-__device__ __forceinline__ float grad_of(float xv, float dy, float mean, float rstd, float w, float b, float &xhat)
-{
-#pragma clang fp contract(off)
-    xhat = (xv - mean) * rstd;
-    const float z = xhat * w + b;
-    if (ACT == 1) return z > 0.0f ? dy : 0.0f;
-    if (ACT == 2) {
-        const float s = sigmoid(z);
-        return dy * (s * fmaf(z, 1.0f - s, 1.0f));
+// Gradient of one channel's values.  With xc = x - mean: xhat = xc rstd, S1 = rstd sum dz xc, and
+// dx = rstd weight dz - xc rstd^2 mean(d xhat) - rstd mean(d), two fused operations.  z is one too, but for a
+// ReLU it takes its formula's operations one at a time, unfused, so that the side of the corner on which a
+// value lies is the formula's own.
+template <bool VEC>
+struct Channels {
+    float w[8], b[8];  // weight and bias
+    PerGroup<VEC> m, r;
+    float rw[8];
+
+    __device__ __forceinline__ void set(const PerGroup<VEC> &mean, const PerGroup<VEC> &rstd)
+    {
+        m = mean;
+        r = rstd;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rw[e] = rstd.get(e) * w[e];
     }
-    return dy;
-}
+    // dz and xc of a value of channel e
+    template <int ACT>
+    __device__ __forceinline__ float dz(float x, float dy, int e, float &xc) const
+    {
+        xc = x - m.get(e);
+        if (ACT == 1) {
+#pragma clang fp contract(off)
+            const float h = xc * r.get(e);
+            const float wh = h * w[e];
+            return wh + b[e] > 0.0f ? dy : 0.0f;
+        }
+        if (ACT == 2) {
+            const float z = fmaf(xc, rw[e], b[e]);
+            const float s = sigmoid(z);
+            return dy * (s * fmaf(z, 1.0f - s, 1.0f));
+        }
+        return dy;
+    }
+};
 
 // Channel sums over the pixel lanes: of the active threads' s1 and s2 the sums [2][tcv * 8], left at the start
 // of red (T * 16 values); part: T values.  Several threads add up one channel where there are
@@ -111,23 +132,28 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
     m.set(p, s, a, [&](int g) { return a.mean[stat + g]; });
     r.set(p, s, a, [&](int g) { return a.rstd[stat + g]; });
     __syncthreads();
-    {
-        float w[8], b[8], s1[8] = {}, s2[8] = {};
+    auto channels = [&]() __attribute__((always_inline)) {
+        Channels<VEC> ch;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            w[e] = pw[p.vec * 8 + e];
-            b[e] = pb[p.vec * 8 + e];
+            ch.w[e] = pw[p.vec * 8 + e];
+            ch.b[e] = pb[p.vec * 8 + e];
         }
+        ch.set(m, r);
+        return ch;
+    };
+    {
+        const Channels<VEC> ch = channels();
+        float s1[8] = {}, s2[8] = {};
         with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (p.pl + i * p.tp >= a.hw) break;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float xhat;
-                    const float dz = grad_of<decltype(act)::value>(raw[i].get(e), draw[i].get(e), m.get(e), r.get(e), w[e],
-                                                                   b[e], xhat);
-                    s1[e] = fmaf(dz, xhat, s1[e]);
+                    float xc;
+                    const float dz = ch.template dz<decltype(act)::value>(raw[i].get(e), draw[i].get(e), e, xc);
+                    s1[e] = fmaf(dz, xc, s1[e]);
                     s2[e] += dz;
                 }
             }
@@ -137,6 +163,8 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
             raw[i].forget();
             draw[i].forget();
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s1[e] *= r.get(e);
         channel_sums<T>(s1, s2, p, red, part);
     }
     const int width = p.tcv * 8;
@@ -149,15 +177,16 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
     weighted_sums<T>(red, width, pw, s, a, [&](int half, int g, float f) { gs[half][g] = f * inv; });
     __syncthreads();
     if (!p.active) return;
-    float w[8], b[8];  // read again: kept across the sums they would cost registers that the slab needs
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        w[e] = pw[p.vec * 8 + e];
-        b[e] = pb[p.vec * 8 + e];
-    }
-    PerGroup<VEC> c1, c2;
+    // the parameters read again: kept across the sums they would cost registers that the slab needs
+    const Channels<VEC> ch = channels();
+    PerGroup<VEC> c1, c2;  // rstd^2 mean(d xhat), rstd mean(d)
     c1.set(p, s, a, [&](int g) { return gs[0][g]; });
     c2.set(p, s, a, [&](int g) { return gs[1][g]; });
+#pragma unroll
+    for (int e = 0; e < (VEC ? 1 : 8); ++e) {
+        c1.v[e] *= r.v[e] * r.v[e];
+        c2.v[e] *= r.v[e];
+    }
     E *dst = (E *)a.y + first * a.ld_y + s.c0 + p.vec * 8;
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
@@ -167,10 +196,9 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float xhat;
-                const float dz = grad_of<decltype(act)::value>(raw[i].get(e), draw[i].get(e), m.get(e), r.get(e), w[e], b[e],
-                                                               xhat);
-                f[e] = r.get(e) * (fmaf(dz, w[e], -c2.get(e)) - xhat * c1.get(e));
+                float xc;
+                const float dz = ch.template dz<decltype(act)::value>(raw[i].get(e), draw[i].get(e), e, xc);
+                f[e] = fmaf(dz, ch.rw[e], fmaf(-xc, c1.get(e), -c2.get(e)));
             }
             store8(dst + (long long)q * a.ld_y, valid, f);
         }
@@ -181,6 +209,22 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
 // Split form: channel sums of a chunk to ws[sample][chunk][2][c], the groups' sums of d xhat and d to
 // gsum[sample][chunk][group][2]; then dx from the groups' joined sums.
 // ------------------------------------------------------------------------------------------
+__device__ __forceinline__ Channels<false> all_channels(const Place &p, const Slab &s, const GnArgs &a, long long stat)
+{
+    Channels<false> ch;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int i = min(p.vec * 8 + e, a.c - 1);
+        ch.w[e] = a.weight ? a.weight[i] : 1.0f;
+        ch.b[e] = a.bias ? a.bias[i] : 0.0f;
+    }
+    PerGroup<false> m, r;
+    m.set(p, s, a, [&](int g) { return a.mean[stat + g]; });
+    r.set(p, s, a, [&](int g) { return a.rstd[stat + g]; });
+    ch.set(m, r);
+    return ch;
+}
+
 template <int T, int TYPE>
 __global__ __launch_bounds__(T) void gn_grad_sums_kernel(GnArgs a)
 {
@@ -193,30 +237,32 @@ __global__ __launch_bounds__(T) void gn_grad_sums_kernel(GnArgs a)
     if (p.active) {
         const long long first = (long long)s.n * a.hw, stat = (long long)s.n * a.groups;
         const Pixels<E> x(a.x, a, a.ld_x), dy(a.dy, a, a.ld_dy);
-        float w[8], b[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int ch = min(p.vec * 8 + e, a.c - 1);
-            w[e] = a.weight ? a.weight[ch] : 1.0f;
-            b[e] = a.bias ? a.bias[ch] : 0.0f;
-        }
-        PerGroup<false> m, r;
-        m.set(p, s, a, [&](int g) { return a.mean[stat + g]; });
-        r.set(p, s, a, [&](int g) { return a.rstd[stat + g]; });
+        const Channels<false> ch = all_channels(p, s, a, stat);
         with_act(a.act, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll 2
-            for (int q = s.p0 + p.pl; q < s.p1; q += p.tp) {
-                const Oct<E> raw = x.get(first + q, p.vec * 8, valid), draw = dy.get(first + q, p.vec * 8, valid);
+            constexpr int AHEAD = T == 1024 ? 2 : 4;  // pixels in flight
+            for (int q = s.p0 + p.pl; q < s.p1; q += AHEAD * p.tp) {
+                Oct<E> raw[AHEAD], draw[AHEAD];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float xhat;
-                    const float dz = grad_of<decltype(act)::value>(raw.get(e), draw.get(e), m.get(e), r.get(e), w[e], b[e],
-                                                                   xhat);
-                    s1[e] = fmaf(dz, xhat, s1[e]);
-                    s2[e] += dz;
+                for (int i = 0; i < AHEAD; ++i)
+                    if (q + i * p.tp < s.p1) {
+                        raw[i] = x.get(first + q + i * p.tp, p.vec * 8, valid);
+                        draw[i] = dy.get(first + q + i * p.tp, p.vec * 8, valid);
+                    }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (q + i * p.tp >= s.p1) break;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float xc;
+                        const float dz = ch.template dz<decltype(act)::value>(raw[i].get(e), draw[i].get(e), e, xc);
+                        s1[e] = fmaf(dz, xc, s1[e]);
+                        s2[e] += dz;
+                    }
                 }
             }
         });
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s1[e] *= ch.r.get(e);
     }
     channel_sums<T>(s1, s2, p, red, part);
     const int width = p.tcv * 8;
@@ -238,63 +284,87 @@ __global__ __launch_bounds__(T) void gn_grad_sums_kernel(GnArgs a)
     }
 }
 
+// The chunks' sums of sample n added up: the groups' means of d xhat and d.  A lane has all of its chunks'
+// parts in flight at once.
+template <int T>
+__device__ __forceinline__ void join_sums(const GnArgs &a, int n, float *g1, float *g2)
+{
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    const v2f *gsum = (const v2f *)a.gsum + (long long)n * a.chunks * a.groups;
+    const float inv = 1.0f / ((float)a.hw * (float)a.cg);
+    const int sub = (int)threadIdx.x & (a.lpg - 1);
+    for (int g = (int)threadIdx.x / a.lpg; g < a.groups; g += T / a.lpg) {
+        v2f t[kJoin];
+        float x1 = 0.0f, x2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            const int k = sub + i * a.lpg;
+            t[i] = k < a.chunks ? gsum[k * a.groups + g] : (v2f){0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            x1 += t[i].x;
+            x2 += t[i].y;
+        }
+        x1 = lanes_sum(x1, a.lpg);
+        x2 = lanes_sum(x2, a.lpg);
+        if (sub == 0) {
+            g1[g] = x1 * inv;
+            g2[g] = x2 * inv;
+        }
+    }
+    __syncthreads();
+}
+
 template <int T, int TYPE>
 __global__ __launch_bounds__(T) void gn_grad_apply_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
-    typedef float v2f __attribute__((ext_vector_type(2)));
     __shared__ float g1[T * 8], g2[T * 8];
+    constexpr int AHEAD = T == 1024 ? 1 : 2;  // pixels in flight
     const Chunk s = chunk_of(a);
-    {
-        const v2f *gsum = (const v2f *)a.gsum + (long long)s.n * a.chunks * a.groups;
-        const float inv = 1.0f / ((float)a.hw * (float)a.cg);
-        const int sub = (int)threadIdx.x & (a.lpg - 1);
-        for (int g = (int)threadIdx.x / a.lpg; g < a.groups; g += T / a.lpg) {
-            float x1 = 0.0f, x2 = 0.0f;
-#pragma unroll 8
-            for (int i = sub; i < a.chunks; i += a.lpg) {
-                const v2f t = gsum[i * a.groups + g];
-                x1 += t.x;
-                x2 += t.y;
-            }
-            x1 = lanes_sum(x1, a.lpg);
-            x2 = lanes_sum(x2, a.lpg);
-            if (sub == 0) {
-                g1[g] = x1 * inv;
-                g2[g] = x2 * inv;
-            }
-        }
-        __syncthreads();
-    }
     const Place p = place<T>((a.c + 7) / 8);
-    if (!p.active) return;
     const int valid = a.c - p.vec * 8;
     const long long first = (long long)s.n * a.hw, stat = (long long)s.n * a.groups;
     const Pixels<E> x(a.x, a, a.ld_x), dy(a.dy, a, a.ld_dy);
-    E *dst = (E *)a.y + first * a.ld_y + p.vec * 8;
-    float w[8], b[8];
+    Oct<E> raw[AHEAD], draw[AHEAD];
+    auto request = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int ch = min(p.vec * 8 + e, a.c - 1);
-        w[e] = a.weight ? a.weight[ch] : 1.0f;
-        b[e] = a.bias ? a.bias[ch] : 0.0f;
-    }
-    PerGroup<false> m, r, c1, c2;
-    m.set(p, s, a, [&](int g) { return a.mean[stat + g]; });
-    r.set(p, s, a, [&](int g) { return a.rstd[stat + g]; });
+        for (int i = 0; i < AHEAD; ++i)
+            if (p.active && q + i * p.tp < s.p1) {
+                raw[i] = x.get(first + q + i * p.tp, p.vec * 8, valid);
+                draw[i] = dy.get(first + q + i * p.tp, p.vec * 8, valid);
+            }
+    };
+    if (T == 1024) join_sums<T>(a, s.n, g1, g2);  // first here: 128 registers do not hold both
+    request(s.p0 + p.pl);
+    const Channels<false> ch = all_channels(p, s, a, stat);
+    if (T != 1024) join_sums<T>(a, s.n, g1, g2);
+    if (!p.active) return;
+    PerGroup<false> c1, c2;  // rstd^2 mean(d xhat), rstd mean(d)
     c1.set(p, s, a, [&](int g) { return g1[g]; });
     c2.set(p, s, a, [&](int g) { return g2[g]; });
-    with_act(a.act, [&](auto act) __attribute__((always_inline)) {
-        for (int q = s.p0 + p.pl; q < s.p1; q += p.tp) {
-            const Oct<E> raw = x.get(first + q, p.vec * 8, valid), draw = dy.get(first + q, p.vec * 8, valid);
-            float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float xhat;
-                const float dz = grad_of<decltype(act)::value>(raw.get(e), draw.get(e), m.get(e), r.get(e), w[e], b[e], xhat);
-                f[e] = r.get(e) * (fmaf(dz, w[e], -c2.get(e)) - xhat * c1.get(e));
+    for (int e = 0; e < 8; ++e) {
+        c1.v[e] *= ch.r.v[e] * ch.r.v[e];
+        c2.v[e] *= ch.r.v[e];
+    }
+    E *dst = (E *)a.y + first * a.ld_y + p.vec * 8;
+    with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+        for (int q = s.p0 + p.pl; q < s.p1; q += AHEAD * p.tp) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (q + i * p.tp >= s.p1) break;
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float xc;
+                    const float dz = ch.template dz<decltype(act)::value>(raw[i].get(e), draw[i].get(e), e, xc);
+                    f[e] = fmaf(dz, ch.rw[e], fmaf(-xc, c1.get(e), -c2.get(e)));
+                }
+                store8(dst + (long long)(q + i * p.tp) * a.ld_y, valid, f);
             }
-            store8(dst + (long long)q * a.ld_y, valid, f);
+            request(q + AHEAD * p.tp);
         }
     });
 }
@@ -354,9 +424,9 @@ hipError_t launch_group_norm_grad(GnArgs a, float *dweight, float *dbias, hipStr
     } else if (rows > 0) {
         const dim3 grid((unsigned)rows);
         a.gsum = a.ws + (size_t)rows * a.c * 2;
-        const bool small = p.threads == 256;
-        GnKernel sums = small ? IFX_GN_TYPES(gn_grad_sums_kernel, 256) : IFX_GN_TYPES(gn_grad_sums_kernel, 1024);
-        GnKernel apply = small ? IFX_GN_TYPES(gn_grad_apply_kernel, 256) : IFX_GN_TYPES(gn_grad_apply_kernel, 1024);
+        const bool small = p.threads == 512;
+        GnKernel sums = small ? IFX_GN_TYPES(gn_grad_sums_kernel, 512) : IFX_GN_TYPES(gn_grad_sums_kernel, 1024);
+        GnKernel apply = small ? IFX_GN_TYPES(gn_grad_apply_kernel, 512) : IFX_GN_TYPES(gn_grad_apply_kernel, 1024);
         hipLaunchKernelGGL(sums, grid, block, 0, s, a);
         hipLaunchKernelGGL(apply, grid, block, 0, s, a);
     }
