@@ -9,6 +9,9 @@
 // vector units: about 20 operations a value with SiLU, whose exponential and reciprocal cost four
 // each.  Hence the activation chosen outside the loops, and z as one fused multiply-add of a
 // 16-bit x, whose own rounding is far coarser than the product's.
+#include <algorithm>
+#include <iterator>
+
 #include "norm_common.h"
 
 namespace ifx {
@@ -329,15 +332,18 @@ int sum_lanes(int groups, int threads)
     return lanes;
 }
 
-// A chunk gives every thread at least one batch, a lane of the join has at most kJoin chunks, and there are
-// about 1024 workgroups where the work allows it.
+// A chunk gives every thread at least one batch (one pixel where that leaves fewer than 256 workgroups), a lane
+// of the join has at most kJoin chunks, and there are about 1024 workgroups where the work allows it.
 Plan plan_split(int n, int hw, int c, int groups)
 {
     Plan p = {};
     p.threads = c <= 2048 ? 512 : 1024;
     const int tp = p.threads / ((c + 7) / 8);
-    const int most = (hw + kBatch * tp - 1) / (kBatch * tp);
+    int most = (hw + kBatch * tp - 1) / (kBatch * tp);
     const int want = n > 0 ? (1024 + n - 1) / n : 1;
+    // few chunks: one pixel a thread before idle CUs
+    if ((long long)n * most < 256) most = std::min((hw + tp - 1) / tp, 256 / (n > 0 ? n : 1));
+    if (most < 1) most = 1;
     int chunks = want < most ? want : most;
     const int limit = kJoin * sum_lanes(groups, p.threads);
     if (chunks > limit) chunks = limit;
@@ -352,7 +358,7 @@ struct Variant {
     int threads, nv;
 };
 constexpr Variant kSlab[] = {{256, 2}, {256, 8}, {512, 8}, {512, 16}, {1024, 16}};
-constexpr Variant kGradSlab[] = {{256, 2}, {256, 4}, {512, 4}, {512, 8}, {1024, 8}};
+constexpr Variant kGradSlab[] = {{256, 2}, {256, 4}, {512, 4}, {1024, 2}, {512, 8}, {1024, 8}};
 
 template <int T, int NV, bool MX4, bool VEC>
 GnKernel slab_kernel(int type)
@@ -400,10 +406,12 @@ Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
         if ((long long)n * (groups / gs) > (1 << 20)) break;  // the grid
         const bool enough = n == 0 || (long long)n * (groups / gs) >= cus;
         if (best.nv && ((least < 64 && best.spans * (long long)n >= cus) || best.gs == gs)) break;
-        for (const Variant &v : grad ? kGradSlab : kSlab)
-            if (v.nv <= most && tcv <= v.threads / 4 && (long long)v.threads / tcv * v.nv >= hw) {
-                best.threads = v.threads;
-                best.nv = v.nv;
+        const Variant *v = grad ? std::begin(kGradSlab) : std::begin(kSlab);
+        const Variant *const end = grad ? std::end(kGradSlab) : std::end(kSlab);
+        for (; v != end; ++v)
+            if (v->nv <= most && tcv <= v->threads / 4 && (long long)v->threads / tcv * v->nv >= hw) {
+                best.threads = v->threads;
+                best.nv = v->nv;
                 best.gs = gs;
                 best.spans = groups / gs;
                 break;

@@ -406,6 +406,8 @@ GnKernel grad_slab_kernel_of(const Plan &p, int type)
     if constexpr (VEC) {
         if (p.threads == 1024) return grad_slab_kernel<1024, 8, VEC>(type);
         if (p.nv == 8) return grad_slab_kernel<512, 8, VEC>(type);
+    } else if (p.threads == 1024) {
+        return gn_grad_slab_kernel<1024, 2, 0, VEC>;  // float: 16-bit types have {512, 4}
     }
     return grad_slab_kernel<512, 4, VEC>(type);
 }
