@@ -16,8 +16,9 @@ import torch
 # Images per pass of ifx_net_forward used by the benchmark (0 = whole batch).
 DEFAULT_SUB_BATCH = 0
 
-from . import (INPUT_NHWC, BlockParams, ConvDesc, NetGraph, NetParams, block_forward, block_workspace_bytes, conv_desc, conv_fused,
-               conv_out_dims, net_forward, net_workspace_bytes, pack_act, pack_weights, synth)
+from . import (ACT_NONE, ACT_SILU, INPUT_NHWC, BlockParams, ConvDesc, NetGraph, NetParams, block_forward, block_workspace_bytes,
+               conv_desc, conv_fused, conv_out_dims, dequantize_i32, group_norm, group_norm_backward, group_norm_mx4, mx4_matmul,
+               mx4_quantize, net_forward, net_workspace_bytes, pack_act, pack_weights, synth)
 
 
 @dataclass
@@ -136,3 +137,42 @@ class DeviceNet:
 
 def pack_input(x_nhwc: torch.Tensor, stream=None) -> torch.Tensor:
     return pack_act(x_nhwc.contiguous(), stream=stream)
+
+
+class NormPointwise4:
+    """A 4-bit pointwise layer behind an int8 convolution: the convolution's int32 accumulators (OUT_I32,
+    channels last), dequantised, group-normalised, activated and rounded to 4 bits, times 4-bit weights.
+
+    weight float [c_out, c] is rounded once; norm_weight, norm_bias float32 [c]; bias float32 [c_out] or
+    None.  forward() serves; norm() and norm_backward() are the layer's normalisation alone with its gradient,
+    for fitting norm_weight and norm_bias to the quantised features.
+    """
+
+    def __init__(self, weight: torch.Tensor, norm_weight: torch.Tensor, norm_bias: torch.Tensor, groups: int,
+                 scale: float, bias: Optional[torch.Tensor] = None, act: int = ACT_SILU, out_act: int = ACT_NONE,
+                 eps: float = 1e-5):
+        self.weight = mx4_quantize(weight)
+        self.norm_weight, self.norm_bias, self.bias = norm_weight, norm_bias, bias
+        self.groups, self.scale, self.act, self.out_act, self.eps = groups, scale, act, out_act, eps
+
+    def features(self, acc: torch.Tensor, stream=None) -> torch.Tensor:
+        """float32 features of int32 accumulators [n, h, w, c]."""
+        return dequantize_i32(acc, self.scale, stream=stream)
+
+    def forward(self, acc: torch.Tensor, residual: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
+                stream=None) -> torch.Tensor:
+        """[n, h, w, c_out] from int32 accumulators [n, h, w, c]; residual of the output's shape and type."""
+        q = group_norm_mx4(self.features(acc, stream), self.groups, self.norm_weight, self.norm_bias, self.eps, self.act,
+                           stream=stream)
+        if residual is not None:
+            residual = residual.view(q.rows, -1)
+        y = mx4_matmul(q, self.weight, self.bias, residual, self.out_act, dtype, stream=stream)
+        return y.view(*acc.shape[:-1], -1)
+
+    def norm(self, x: torch.Tensor, stream=None):
+        """(y, mean, rstd) of the normalisation alone."""
+        return group_norm(x, self.groups, self.norm_weight, self.norm_bias, self.eps, self.act, stream=stream)
+
+    def norm_backward(self, dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, stream=None):
+        """(dx, dweight, dbias) of norm()."""
+        return group_norm_backward(dy, x, mean, rstd, self.groups, self.norm_weight, self.norm_bias, self.act, stream=stream)
