@@ -65,17 +65,26 @@ struct Words<4> {
 };
 
 template <typename E>
-__device__ __forceinline__ Oct<E> load8(const E *p, int valid)
+__device__ __forceinline__ Oct<E> load8(const E *p)
 {
     typedef typename Words<sizeof(E)>::type V;
     Oct<E> o;
+#pragma unroll
+    for (int i = 0; i < Oct<E>::W / 4; ++i) {
+        const V v = ((const V *)p)[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.w[4 * i + j] = v[j];
+    }
+    return o;
+}
+
+// The first `valid` of eight values, the others 0.
+template <typename E>
+__device__ __forceinline__ Oct<E> load8(const E *p, int valid)
+{
+    Oct<E> o;
     if (valid >= 8) {
-#pragma unroll
-        for (int i = 0; i < Oct<E>::W / 4; ++i) {
-            const V v = ((const V *)p)[i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o.w[4 * i + j] = v[j];
-        }
+        o = load8(p);
     } else {
 #pragma unroll
         for (int i = 0; i < Oct<E>::W; ++i) o.w[i] = 0;
@@ -100,16 +109,22 @@ __device__ __forceinline__ unsigned pack2(float a, float b)
 }
 
 template <typename E>
-__device__ __forceinline__ void store8(E *p, int valid, const float (&f)[8])
+__device__ __forceinline__ void store8(E *p, const float (&f)[8])
 {
     typedef typename Words<sizeof(E)>::type V;
+    if constexpr (sizeof(E) == 4) {
+        ((V *)p)[0] = (V){__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+        ((V *)p)[1] = (V){__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
+    } else {
+        *(V *)p = (V){pack2<E>(f[0], f[1]), pack2<E>(f[2], f[3]), pack2<E>(f[4], f[5]), pack2<E>(f[6], f[7])};
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ void store8(E *p, int valid, const float (&f)[8])
+{
     if (valid >= 8) {
-        if constexpr (sizeof(E) == 4) {
-            ((V *)p)[0] = (V){__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-            ((V *)p)[1] = (V){__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
-        } else {
-            *(V *)p = (V){pack2<E>(f[0], f[1]), pack2<E>(f[2], f[3]), pack2<E>(f[4], f[5]), pack2<E>(f[6], f[7])};
-        }
+        store8(p, f);
     } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
@@ -122,6 +137,20 @@ __device__ __forceinline__ void store8(E *p, int valid, const float (&f)[8])
 __device__ __forceinline__ float sigmoid(float z)
 {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+}
+
+// The activation of z / pre_scale<ACT>(): SiLU takes z log2(e), which spares the exponential's product.
+template <int ACT>
+__device__ __forceinline__ constexpr float pre_scale()
+{
+    return ACT == 2 ? 1.44269504f : 1.0f;
+}
+template <int ACT>
+__device__ __forceinline__ float act_scaled(float z)
+{
+    if (ACT == 1) return z < 0.0f ? 0.0f : z;
+    if (ACT == 2) return z * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_exp2f(-z), 1.44269504f, 1.44269504f));
+    return z;
 }
 
 template <int ACT>

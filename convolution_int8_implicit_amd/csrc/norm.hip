@@ -31,35 +31,71 @@ struct Affine {
             if (TYPE != 0) b[e] = fmaf(-mean.get(e), w[e], b[e]);
         }
     }
+    template <int ACT>
+    __device__ __forceinline__ void scale()
+    {
+        if (ACT == 2)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                w[e] *= pre_scale<ACT>();
+                b[e] *= pre_scale<ACT>();
+            }
+    }
+    // pre_scale times it, after scale()
     __device__ __forceinline__ float z(float x, int e) const
     {
         return TYPE == 0 ? fmaf(x - m.get(e), w[e], b[e]) : fmaf(x, w[e], b[e]);
     }
 };
 
-// Eight normalised channels of pixel `row`, from channel ch on, stored or rounded.
-template <int ACT, int TYPE, bool MX4, bool VEC>
-__device__ __forceinline__ void put_pixel(const Oct<typename Elem<TYPE>::type> &raw, const Affine<TYPE, VEC> &f, long long row,
-                                          int ch, int valid, const GnArgs &a)
-{
+// Where a thread's results go: eight channels from channel ch on of pixels row + i * step.
+template <int TYPE, bool MX4, bool WHOLE>
+struct Results {
     typedef typename Elem<TYPE>::type E;
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = act_of<ACT>(f.z(raw.get(e), e));
-    if (MX4) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e >= valid) y[e] = 0.0f;
-        unsigned sc;
-        const unsigned code = mx4_codes(y, sc);
-        const int vec = ch >> 3;
-        const long long at = (long long)(vec >> 4) * a.n * a.hw + row;
-        ((unsigned *)a.codes)[at * 16 + (vec & 15)] = code;
-        if ((vec & 3) == 0) a.scales[at * 4 + ((vec & 15) >> 2)] = (uint8_t)sc;
-    } else {
-        store8((E *)a.y + row * a.ld_y + ch, valid, y);
+    Pixels<E, WHOLE> y;
+    unsigned *codes;  // of pixel `row`
+    uint8_t *scale;   // of the block, or null in three threads of four
+    int step, valid;
+
+    __device__ __forceinline__ Results(const GnArgs &a, long long row, int step_, int ch, int valid_)
+        : y(a.y, a, a.ld_y, row, step_, ch, valid_), step(step_), valid(valid_)
+    {
+        if (MX4) {
+            const int vec = ch >> 3;
+            const long long at = (long long)(vec >> 4) * a.n * a.hw + row;
+            codes = (unsigned *)a.codes + at * 16 + (vec & 15);
+            scale = (vec & 3) == 0 ? a.scales + at * 4 + ((vec & 15) >> 2) : nullptr;
+        }
     }
-}
+
+    template <int ACT, bool VEC>
+    __device__ __forceinline__ void put(int i, const Oct<E> &raw, const Affine<TYPE, VEC> &f) const
+    {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = act_scaled<ACT>(f.z(raw.get(e), e));
+        if constexpr (MX4) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (WHOLE ? valid <= 0 : e >= valid) v[e] = 0.0f;
+            unsigned sc;
+            const unsigned code = mx4_codes(v, sc);
+            codes[(long long)i * step * 16] = code;
+            if (scale) scale[(long long)i * step * 4] = (uint8_t)sc;
+        } else {
+            y.put(i, v);
+        }
+    }
+    __device__ __forceinline__ void advance(int i)
+    {
+        if constexpr (MX4) {
+            codes += (long long)i * step * 16;
+            if (scale) scale += (long long)i * step * 4;
+        } else {
+            y.advance(i);
+        }
+    }
+};
 
 // ------------------------------------------------------------------------------------------
 // Slab form
@@ -78,16 +114,14 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_slab_kernel(G
     const Place p = place<T>(last ? (a.c + 127) / 128 * 16 - s.c0 / 8 : (s.cs + 7) / 8);
     const int valid = s.cs - p.vec * 8;
     const long long first = (long long)s.n * a.hw;
-    const Pixels<E> x(a.x, a, a.ld_x);
+    const Pixels<E, VEC> x(a.x, a, a.ld_x, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
     Oct<E> raw[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int q = p.pl + i * p.tp;
-        if (p.active && q < a.hw && valid > 0)
-            raw[i] = x.get(first + q, s.c0 + p.vec * 8, valid);
+    for (int i = 0; i < NV; ++i)
+        if (p.active && p.pl + i * p.tp < a.hw && valid > 0)
+            raw[i] = x.get(i);
         else
             raw[i] = {};
-    }
     stage_params<T>(s, a, pw, pb);
     float v[VEC ? 1 : 8] = {};
 #pragma unroll
@@ -141,12 +175,14 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_slab_kernel(G
         f.b[e] = pb[p.vec * 8 + e];
     }
     f.set(m, r);
+    const Results<TYPE, MX4, VEC> y(a, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
+        f.template scale<ACT>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int q = p.pl + i * p.tp;
-            if (q >= a.hw) break;
-            put_pixel<decltype(act)::value, TYPE, MX4, VEC>(raw[i], f, first + q, s.c0 + p.vec * 8, valid, a);
+            if (p.pl + i * p.tp >= a.hw) break;
+            y.template put<ACT>(i, raw[i], f);
         }
     });
 }
@@ -167,7 +203,7 @@ __global__ __launch_bounds__(T) void gn_stats_kernel(GnArgs a)
     const Place p = place<T>((a.c + 7) / 8);
     const int valid = a.c - p.vec * 8;
     const long long first = (long long)s.n * a.hw;
-    const Pixels<E> x(a.x, a, a.ld_x);
+    Pixels<E, VEC> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     int cnt = 0;  // pixels joined
     float mean[P] = {}, m2[P] = {};
     if (p.active) {
@@ -177,9 +213,10 @@ __global__ __launch_bounds__(T) void gn_stats_kernel(GnArgs a)
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const bool in = q + i * p.tp < s.p1;
-                raw[i] = x.get(first + (in ? q + i * p.tp : q), p.vec * 8, valid);
+                raw[i] = x.get(in ? i : 0);
                 have += in;
             }
+            x.advance(kBatch);
             const float each = (float)(VEC ? 8 * have : have), part = (float)have / (float)(cnt + have);
             const float both = (float)(VEC ? 8 * cnt : cnt) * part;
             float sum[P] = {}, sq[P] = {};
@@ -274,20 +311,21 @@ __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
     __shared__ float smean[T * 8], srstd[T * 8];
-    constexpr int AHEAD = 4;  // loads in flight
+    constexpr int AHEAD = T == 1024 ? 2 : 4;  // loads in flight
     const Chunk s = chunk_of(a);
     const Place p = place<T>(MX4 ? (a.c + 127) / 128 * 16 : (a.c + 7) / 8);
     const int valid = a.c - p.vec * 8;
     const long long first = (long long)s.n * a.hw;
-    const Pixels<E> x(a.x, a, a.ld_x);
+    Pixels<E, false> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     Oct<E> raw[AHEAD];
     auto request = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             if (q + i * p.tp < s.p1 && p.active && valid > 0)
-                raw[i] = x.get(first + q + i * p.tp, p.vec * 8, valid);
+                raw[i] = x.get(i);
             else
                 raw[i] = {};
+        x.advance(AHEAD);
     };
     if (T == 1024) join_stats<T>(a, s.n, smean, srstd);  // first here: 128 registers do not hold both
     request(s.p0 + p.pl);
@@ -309,12 +347,15 @@ __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
     m.set(p, s, a, [&](int g) { return smean[g]; });
     r.set(p, s, a, [&](int g) { return srstd[g]; });
     f.set(m, r);
+    Results<TYPE, MX4, false> y(a, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
+        f.template scale<ACT>();
         for (int q = s.p0 + p.pl; q < s.p1; q += AHEAD * p.tp) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
-                if (q + i * p.tp < s.p1)
-                    put_pixel<decltype(act)::value, TYPE, MX4, false>(raw[i], f, first + q + i * p.tp, p.vec * 8, valid, a);
+                if (q + i * p.tp < s.p1) y.template put<ACT>(i, raw[i], f);
+            y.advance(AHEAD);
             request(q + AHEAD * p.tp);
         }
     });

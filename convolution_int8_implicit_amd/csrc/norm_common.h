@@ -81,29 +81,45 @@ __device__ __forceinline__ Place place(int tcv)
 {
     Place p;
     p.tcv = tcv;
-    p.tp = T / tcv;
+    p.tp = __builtin_amdgcn_readfirstlane(T / tcv);
     p.pl = (int)threadIdx.x / tcv;
     p.vec = (int)threadIdx.x - p.pl * tcv;
     p.active = p.pl < p.tp;
     return p;
 }
 
-// A tensor of n * hw pixels: eight channels from channel ch of pixel `row` on, of which `valid` are the
-// caller's.  The others' values are arbitrary: where memory goes on behind them (the next pixel) they
-// are read too, so only a tensor's very last vector is read value by value.
-template <typename E>
+// A thread's view of a tensor of n * hw pixels: eight channels from channel ch on of the pixels row + i * step, of
+// which `valid` are the caller's (WHOLE: all).  The others' values are arbitrary: where memory goes on
+// behind them (the next pixel) they are read too, so only a tensor's very last vector is read value by
+// value.  The start is one 64-bit product, a pixel's address one addition of a uniform stride.
+template <typename E, bool WHOLE>
 struct Pixels {
-    const E *base, *end;
-    long long ld;
-    __device__ __forceinline__ Pixels(const void *p, const GnArgs &a, long long ld_)
-        : base((const E *)p), end((const E *)p + ((long long)a.n * a.hw - 1) * ld_ + a.c), ld(ld_)
+    const E *at, *end;
+    long long stride;
+    int valid;
+    __device__ __forceinline__ Pixels(const void *p, const GnArgs &a, long long ld, long long row, int step, int ch, int valid_)
+        : at((const E *)p + row * ld + ch), end((const E *)p + ((long long)a.n * a.hw - 1) * ld + a.c), stride(step * ld),
+          valid(valid_)
     {
     }
-    __device__ __forceinline__ Oct<E> get(long long row, int ch, int valid) const
+    __device__ __forceinline__ Oct<E> get(int i) const
     {
-        const E *p = base + row * ld + ch;
-        return load8(p, p + 8 <= end ? 8 : valid);
+        const E *p = at + i * stride;
+        if constexpr (WHOLE)
+            return load8(p);
+        else
+            return load8(p, p + 8 <= end ? 8 : valid);
     }
+    __device__ __forceinline__ void put(int i, const float (&f)[8]) const
+    {
+        E *p = const_cast<E *>(at) + i * stride;
+        if constexpr (WHOLE)
+            store8(p, f);
+        else
+            store8(p, valid, f);
+    }
+    // on by i steps
+    __device__ __forceinline__ void advance(int i) { at += i * stride; }
 };
 
 template <int CTRL>

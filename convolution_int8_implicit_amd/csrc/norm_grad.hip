@@ -113,18 +113,19 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
     const Place p = place<T>((s.cs + 7) / 8);
     const int valid = s.cs - p.vec * 8;
     const long long first = (long long)s.n * a.hw;
-    const Pixels<E> x(a.x, a, a.ld_x), dy(a.dy, a, a.ld_dy);
     Oct<E> raw[NV], draw[NV];
+    {
+        const Pixels<E, VEC> x(a.x, a, a.ld_x, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
+        const Pixels<E, VEC> dy(a.dy, a, a.ld_dy, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int q = p.pl + i * p.tp;
-        if (p.active && q < a.hw) {
-            raw[i] = x.get(first + q, s.c0 + p.vec * 8, valid);
-            draw[i] = dy.get(first + q, s.c0 + p.vec * 8, valid);
-        } else {
-            raw[i] = {};
-            draw[i] = {};
-        }
+        for (int i = 0; i < NV; ++i)
+            if (p.active && p.pl + i * p.tp < a.hw) {
+                raw[i] = x.get(i);
+                draw[i] = dy.get(i);
+            } else {
+                raw[i] = {};
+                draw[i] = {};
+            }
     }
     stage_params<T>(s, a, pw, pb);
     const long long stat = (long long)s.n * a.groups + s.g0;
@@ -187,12 +188,11 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
         c1.v[e] *= r.v[e] * r.v[e];
         c2.v[e] *= r.v[e];
     }
-    E *dst = (E *)a.y + first * a.ld_y + s.c0 + p.vec * 8;
+    const Pixels<E, VEC> dx(a.y, a, a.ld_y, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int q = p.pl + i * p.tp;
-            if (q >= a.hw) break;
+            if (p.pl + i * p.tp >= a.hw) break;
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
                 const float dz = ch.template dz<decltype(act)::value>(raw[i].get(e), draw[i].get(e), e, xc);
                 f[e] = fmaf(dz, ch.rw[e], fmaf(-xc, c1.get(e), -c2.get(e)));
             }
-            store8(dst + (long long)q * a.ld_y, valid, f);
+            dx.put(i, f);
         }
     });
 }
@@ -236,7 +236,8 @@ __global__ __launch_bounds__(T) void gn_grad_sums_kernel(GnArgs a)
     float s1[8] = {}, s2[8] = {};
     if (p.active) {
         const long long first = (long long)s.n * a.hw, stat = (long long)s.n * a.groups;
-        const Pixels<E> x(a.x, a, a.ld_x), dy(a.dy, a, a.ld_dy);
+        Pixels<E, false> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+        Pixels<E, false> dy(a.dy, a, a.ld_dy, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
         const Channels<false> ch = all_channels(p, s, a, stat);
         with_act(a.act, [&](auto act) __attribute__((always_inline)) {
             constexpr int AHEAD = T == 1024 ? 2 : 4;  // pixels in flight
@@ -245,9 +246,11 @@ __global__ __launch_bounds__(T) void gn_grad_sums_kernel(GnArgs a)
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i)
                     if (q + i * p.tp < s.p1) {
-                        raw[i] = x.get(first + q + i * p.tp, p.vec * 8, valid);
-                        draw[i] = dy.get(first + q + i * p.tp, p.vec * 8, valid);
+                        raw[i] = x.get(i);
+                        draw[i] = dy.get(i);
                     }
+                x.advance(AHEAD);
+                dy.advance(AHEAD);
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
                     if (q + i * p.tp >= s.p1) break;
@@ -326,15 +329,19 @@ __global__ __launch_bounds__(T) void gn_grad_apply_kernel(GnArgs a)
     const Place p = place<T>((a.c + 7) / 8);
     const int valid = a.c - p.vec * 8;
     const long long first = (long long)s.n * a.hw, stat = (long long)s.n * a.groups;
-    const Pixels<E> x(a.x, a, a.ld_x), dy(a.dy, a, a.ld_dy);
+    Pixels<E, false> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, false> dy(a.dy, a, a.ld_dy, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, false> dx(a.y, a, a.ld_y, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     Oct<E> raw[AHEAD], draw[AHEAD];
     auto request = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             if (p.active && q + i * p.tp < s.p1) {
-                raw[i] = x.get(first + q + i * p.tp, p.vec * 8, valid);
-                draw[i] = dy.get(first + q + i * p.tp, p.vec * 8, valid);
+                raw[i] = x.get(i);
+                draw[i] = dy.get(i);
             }
+        x.advance(AHEAD);
+        dy.advance(AHEAD);
     };
     if (T == 1024) join_sums<T>(a, s.n, g1, g2);  // first here: 128 registers do not hold both
     request(s.p0 + p.pl);
@@ -349,7 +356,6 @@ __global__ __launch_bounds__(T) void gn_grad_apply_kernel(GnArgs a)
         c1.v[e] *= ch.r.v[e] * ch.r.v[e];
         c2.v[e] *= ch.r.v[e];
     }
-    E *dst = (E *)a.y + first * a.ld_y + p.vec * 8;
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
         for (int q = s.p0 + p.pl; q < s.p1; q += AHEAD * p.tp) {
 #pragma unroll
@@ -362,8 +368,9 @@ __global__ __launch_bounds__(T) void gn_grad_apply_kernel(GnArgs a)
                     const float dz = ch.template dz<decltype(act)::value>(raw[i].get(e), draw[i].get(e), e, xc);
                     f[e] = fmaf(dz, ch.rw[e], fmaf(-xc, c1.get(e), -c2.get(e)));
                 }
-                store8(dst + (long long)(q + i * p.tp) * a.ld_y, valid, f);
+                dx.put(i, f);
             }
+            dx.advance(AHEAD);
             request(q + AHEAD * p.tp);
         }
     });
