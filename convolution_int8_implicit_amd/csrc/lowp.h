@@ -176,10 +176,8 @@ __device__ __forceinline__ void with_act(int act, F f)
 // Maximum over the four lanes 4i .. 4i + 3 (every lane of the wave active).
 __device__ __forceinline__ unsigned quad_max(unsigned u)
 {
-    const unsigned a = (unsigned)__builtin_amdgcn_mov_dpp((int)u, 0xb1, 0xf, 0xf, true);  // lanes 1 0 3 2
-    u = a > u ? a : u;
-    const unsigned b = (unsigned)__builtin_amdgcn_mov_dpp((int)u, 0x4e, 0xf, 0xf, true);  // lanes 2 3 0 1
-    return b > u ? b : u;
+    u = max(u, (unsigned)__builtin_amdgcn_mov_dpp((int)u, 0xb1, 0xf, 0xf, true));  // lanes 1 0 3 2
+    return max(u, (unsigned)__builtin_amdgcn_mov_dpp((int)u, 0x4e, 0xf, 0xf, true));  // lanes 2 3 0 1
 }
 
 // Microscaled 4-bit codes of a block of 32 values held by four neighbouring lanes, eight each
@@ -189,13 +187,12 @@ __device__ __forceinline__ unsigned quad_max(unsigned u)
 // and zero codes.  Returns the lane's eight codes, the lowest column in the lowest bits.
 __device__ __forceinline__ unsigned mx4_codes(const float (&f)[8], unsigned &scale)
 {
-    unsigned u = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const unsigned a = __float_as_uint(f[e]) & 0x7fffffffu;
-        u = a > u ? a : u;
-    }
-    u = quad_max(u) >> 23;
+    // the maximum that keeps a NaN, three operands at a time
+    float top = __builtin_elementwise_maximum(fabsf(f[0]), fabsf(f[1]));
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, fabsf(f[2])), fabsf(f[3]));
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, fabsf(f[4])), fabsf(f[5]));
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, fabsf(f[6])), fabsf(f[7]));
+    const unsigned u = quad_max(__float_as_uint(top)) >> 23 & 255u;
     const bool bad = u == 255u;
     const unsigned s = (u < 2u ? 2u : u) - 2u;
     scale = bad ? 255u : s;
