@@ -78,24 +78,20 @@ __device__ __forceinline__ Oct<E> load8(const E *p)
     return o;
 }
 
-// The first `valid` of eight values, the others 0.
+// The first `valid` >= 1 of eight values; those past them are arbitrary (the last one again).
 template <typename E>
 __device__ __forceinline__ Oct<E> load8(const E *p, int valid)
 {
+    if (valid >= 8) return load8(p);
     Oct<E> o;
-    if (valid >= 8) {
-        o = load8(p);
+    if constexpr (sizeof(E) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o.w[e] = ((const unsigned *)p)[min(e, valid - 1)];
     } else {
 #pragma unroll
-        for (int i = 0; i < Oct<E>::W; ++i) o.w[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-            if (e < valid) {
-                if constexpr (sizeof(E) == 4)
-                    o.w[e] = ((const unsigned *)p)[e];
-                else
-                    o.w[e / 2] |= (unsigned)((const unsigned short *)p)[e] << (16 * (e & 1));
-            }
+        for (int e = 0; e < 4; ++e)
+            o.w[e] = ((const unsigned short *)p)[min(2 * e, valid - 1)] |
+                     (unsigned)((const unsigned short *)p)[min(2 * e + 1, valid - 1)] << 16;
     }
     return o;
 }

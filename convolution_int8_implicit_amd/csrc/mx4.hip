@@ -43,14 +43,19 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *x, long l
 #pragma unroll
     for (int i = 0; i < kQPanels; ++i) {
         const int col = (pg * kQPanels + i) * 128 + v * 8;
-        raw[i] = load8(src + (col < k ? col : 0), k - col);
+        raw[i] = col < k ? load8(src + col, k - col) : Oct<E>{};
     }
 #pragma unroll
     for (int i = 0; i < kQPanels; ++i) {
-        const int p = pg * kQPanels + i;
+        const int p = pg * kQPanels + i, col = p * 128 + v * 8;
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = raw[i].get(e);
+        if (col + 8 > k) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e >= k) f[e] = 0.0f;
+        }
         unsigned s;
         const unsigned r = mx4_codes(f, s);
         if (live && p < k1) {

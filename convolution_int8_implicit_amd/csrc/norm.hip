@@ -100,10 +100,11 @@ struct Results {
 // ------------------------------------------------------------------------------------------
 // Slab form
 // ------------------------------------------------------------------------------------------
-template <int T, int NV, int TYPE, bool MX4, bool VEC>
+template <int T, int NV, int TYPE, bool MX4, Mode MODE>
 __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_slab_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
+    constexpr bool VEC = MODE == kVec, WHOLE = MODE != kRagged;
     constexpr int LDS = T * (VEC ? 1 : 8);
     __shared__ float red[LDS], gs[2 * T];
     __shared__ __attribute__((aligned(16))) float pw[2 * T], pb[2 * T];
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_slab_kernel(G
     const Place p = place<T>(last ? (a.c + 127) / 128 * 16 - s.c0 / 8 : (s.cs + 7) / 8);
     const int valid = s.cs - p.vec * 8;
     const long long first = (long long)s.n * a.hw;
-    const Pixels<E, VEC> x(a.x, a, a.ld_x, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
+    const Pixels<E, WHOLE> x(a.x, a, a.ld_x, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
     Oct<E> raw[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -175,7 +176,7 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_slab_kernel(G
         f.b[e] = pb[p.vec * 8 + e];
     }
     f.set(m, r);
-    const Results<TYPE, MX4, VEC> y(a, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
+    const Results<TYPE, MX4, WHOLE> y(a, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
         constexpr int ACT = decltype(act)::value;
         f.template scale<ACT>();
@@ -192,10 +193,11 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_slab_kernel(G
 // ------------------------------------------------------------------------------------------
 
 // Mean and sum of squares about it of every group over a chunk's pixels, to ws[sample][chunk][group][2].
-template <int T, int TYPE, bool VEC>
+template <int T, int TYPE, Mode MODE>
 __global__ __launch_bounds__(T) void gn_stats_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
+    constexpr bool VEC = MODE == kVec, WHOLE = MODE != kRagged;
     constexpr int LDS = T * (VEC ? 1 : 8);
     constexpr int P = VEC ? 1 : 8;  // parts a thread keeps: of its vector or of each channel
     __shared__ float red[LDS], gs[LDS];
@@ -203,7 +205,7 @@ __global__ __launch_bounds__(T) void gn_stats_kernel(GnArgs a)
     const Place p = place<T>((a.c + 7) / 8);
     const int valid = a.c - p.vec * 8;
     const long long first = (long long)s.n * a.hw;
-    Pixels<E, VEC> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, WHOLE> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     int cnt = 0;  // pixels joined
     float mean[P] = {}, m2[P] = {};
     if (p.active) {
@@ -306,7 +308,7 @@ __device__ __forceinline__ void join_stats(const GnArgs &a, int n, float *smean,
 
 // The chunks joined, then each pixel normalised.  MX4: threads also cover the columns up to the next
 // multiple of 128.  The first pixels and the parameters are requested before the join.
-template <int T, int TYPE, bool MX4>
+template <int T, int TYPE, bool MX4, bool WHOLE>
 __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
     const Place p = place<T>(MX4 ? (a.c + 127) / 128 * 16 : (a.c + 7) / 8);
     const int valid = a.c - p.vec * 8;
     const long long first = (long long)s.n * a.hw;
-    Pixels<E, false> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, WHOLE> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     Oct<E> raw[AHEAD];
     auto request = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
@@ -347,7 +349,7 @@ __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
     m.set(p, s, a, [&](int g) { return smean[g]; });
     r.set(p, s, a, [&](int g) { return srstd[g]; });
     f.set(m, r);
-    Results<TYPE, MX4, false> y(a, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Results<TYPE, MX4, WHOLE> y(a, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
         constexpr int ACT = decltype(act)::value;
         f.template scale<ACT>();
@@ -374,14 +376,15 @@ int sum_lanes(int groups, int threads)
 }
 
 // A chunk gives every thread at least one batch (one pixel where that leaves fewer than 256 workgroups), a lane
-// of the join has at most kJoin chunks, and there are about 1024 workgroups where the work allows it.
+// of the join has at most kJoin chunks, and there are at most 512 workgroups, two on each of 256 CUs, so that
+// they run at once (16 x 2500 x 640: 848 took 48 us, 512 38).
 Plan plan_split(int n, int hw, int c, int groups)
 {
     Plan p = {};
     p.threads = c <= 2048 ? 512 : 1024;
     const int tp = p.threads / ((c + 7) / 8);
     int most = (hw + kBatch * tp - 1) / (kBatch * tp);
-    const int want = n > 0 ? (1024 + n - 1) / n : 1;
+    const int want = n > 0 && n < 512 ? 512 / n : 1;
     // few chunks: one pixel a thread before idle CUs
     if ((long long)n * most < 256) most = std::min((hw + tp - 1) / tp, 256 / (n > 0 ? n : 1));
     if (most < 1) most = 1;
@@ -399,26 +402,50 @@ struct Variant {
     int threads, nv;
 };
 constexpr Variant kSlab[] = {{256, 2}, {256, 8}, {512, 8}, {512, 16}, {1024, 16}};
-constexpr Variant kGradSlab[] = {{256, 2}, {256, 4}, {512, 4}, {1024, 2}, {512, 8}, {1024, 8}};
+constexpr Variant kGradSlab[] = {{256, 2}, {256, 4}, {512, 4}, {1024, 2}, {512, 8}};
 
-template <int T, int NV, bool MX4, bool VEC>
+template <int T, int NV, bool MX4, Mode MODE>
 GnKernel slab_kernel(int type)
 {
     if constexpr (NV <= 8)
-        if (type == 0) return gn_slab_kernel<T, NV, 0, MX4, VEC>;
-    return type == 1 ? gn_slab_kernel<T, NV, 1, MX4, VEC> : gn_slab_kernel<T, NV, 2, MX4, VEC>;
+        if (type == 0) return gn_slab_kernel<T, NV, 0, MX4, MODE>;
+    return type == 1 ? gn_slab_kernel<T, NV, 1, MX4, MODE> : gn_slab_kernel<T, NV, 2, MX4, MODE>;
 }
 
-template <bool MX4, bool VEC>
+template <bool MX4, Mode MODE>
 GnKernel slab_kernel_of(const Plan &p, int type)
 {
     if (p.threads == 256)
-        return p.nv == 2 ? slab_kernel<256, 2, MX4, VEC>(type) : slab_kernel<256, 8, MX4, VEC>(type);
-    if constexpr (VEC) {
-        if (p.threads == 1024) return slab_kernel<1024, 16, MX4, VEC>(type);
-        if (p.nv == 16) return slab_kernel<512, 16, MX4, VEC>(type);
+        return p.nv == 2 ? slab_kernel<256, 2, MX4, MODE>(type) : slab_kernel<256, 8, MX4, MODE>(type);
+    if constexpr (MODE == kVec) {
+        if (p.threads == 1024) return slab_kernel<1024, 16, MX4, MODE>(type);
+        if (p.nv == 16) return slab_kernel<512, 16, MX4, MODE>(type);
     }
-    return slab_kernel<512, 8, MX4, VEC>(type);
+    return slab_kernel<512, 8, MX4, MODE>(type);
+}
+
+template <bool MX4>
+GnKernel slab_kernel_of(const Plan &p, int type, Mode mode)
+{
+    return mode == kVec     ? slab_kernel_of<MX4, kVec>(p, type)
+           : mode == kWhole ? slab_kernel_of<MX4, kWhole>(p, type)
+                            : slab_kernel_of<MX4, kRagged>(p, type);
+}
+
+template <int T>
+GnKernel stats_kernel_of(const GnArgs &a, Mode mode)
+{
+    return mode == kVec     ? IFX_GN_TYPES(gn_stats_kernel, T, kVec)
+           : mode == kWhole ? IFX_GN_TYPES(gn_stats_kernel, T, kWhole)
+                            : IFX_GN_TYPES(gn_stats_kernel, T, kRagged);
+}
+
+template <int T>
+GnKernel apply_kernel_of(const GnArgs &a, bool mx4, Mode mode)
+{
+    if (mx4)
+        return mode != kRagged ? IFX_GN_TYPES(gn_apply_kernel, T, true, true) : IFX_GN_TYPES(gn_apply_kernel, T, true, false);
+    return mode != kRagged ? IFX_GN_TYPES(gn_apply_kernel, T, false, true) : IFX_GN_TYPES(gn_apply_kernel, T, false, false);
 }
 
 }  // namespace
@@ -496,22 +523,16 @@ hipError_t launch_group_norm(GnArgs a, hipStream_t s)
     const Plan p = gn_plan(a.n, a.hw, a.c, a.groups, a.type, false, mx4);
     gn_fill(a, p);
     const dim3 block((unsigned)p.threads);
-    const bool vec = a.cg % 8 == 0;
+    const Mode mode = mode_of(p.nv ? p.gs * a.cg : a.c, a.cg);
     if (p.nv) {
-        GnKernel f = mx4 ? (vec ? slab_kernel_of<true, true>(p, a.type) : slab_kernel_of<true, false>(p, a.type))
-                         : (vec ? slab_kernel_of<false, true>(p, a.type) : slab_kernel_of<false, false>(p, a.type));
+        GnKernel f = mx4 ? slab_kernel_of<true>(p, a.type, mode) : slab_kernel_of<false>(p, a.type, mode);
         hipLaunchKernelGGL(f, dim3((unsigned)a.per_xcd * 8u), block, 0, s, a);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)(a.n * p.chunks));
-    GnKernel stats, apply;
-    if (p.threads == 512) {
-        stats = vec ? IFX_GN_TYPES(gn_stats_kernel, 512, true) : IFX_GN_TYPES(gn_stats_kernel, 512, false);
-        apply = mx4 ? IFX_GN_TYPES(gn_apply_kernel, 512, true) : IFX_GN_TYPES(gn_apply_kernel, 512, false);
-    } else {
-        stats = vec ? IFX_GN_TYPES(gn_stats_kernel, 1024, true) : IFX_GN_TYPES(gn_stats_kernel, 1024, false);
-        apply = mx4 ? IFX_GN_TYPES(gn_apply_kernel, 1024, true) : IFX_GN_TYPES(gn_apply_kernel, 1024, false);
-    }
+    const bool wide = p.threads == 1024;
+    GnKernel stats = wide ? stats_kernel_of<1024>(a, mode) : stats_kernel_of<512>(a, mode);
+    GnKernel apply = wide ? apply_kernel_of<1024>(a, mx4, mode) : apply_kernel_of<512>(a, mx4, mode);
     hipLaunchKernelGGL(stats, grid, block, 0, s, a);
     hipLaunchKernelGGL(apply, grid, block, 0, s, a);
     return hipGetLastError();

@@ -30,6 +30,14 @@ constexpr int kJoin = 16;    // chunks' parts that a lane joins at most
 // Device side
 // ------------------------------------------------------------------------------------------
 
+// What a kernel may take for granted of its threads' vectors of eight channels.
+enum Mode {
+    kRagged,  // the last one may hold fewer of the workgroup's channels
+    kWhole,   // all eight are the workgroup's (cs is a multiple of 8)
+    kVec      // and all eight of one group (cg is a multiple of 8)
+};
+inline Mode mode_of(int cs, int cg) { return cg % 8 == 0 ? kVec : cs % 8 == 0 ? kWhole : kRagged; }
+
 // The groups and channels a workgroup covers, and its sample.
 struct Slab {
     int n, g0, ng, c0, cs;  // sample, first group, groups, first channel, channels

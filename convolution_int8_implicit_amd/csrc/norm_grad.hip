@@ -102,10 +102,11 @@ __device__ __forceinline__ void weighted_sums(const float *sums, int width, cons
 // ------------------------------------------------------------------------------------------
 // Slab form: x and dy in registers; channel sums to ws[sample][2][c].
 // ------------------------------------------------------------------------------------------
-template <int T, int NV, int TYPE, bool VEC>
+template <int T, int NV, int TYPE, Mode MODE>
 __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
+    constexpr bool VEC = MODE == kVec, WHOLE = MODE != kRagged;
     __shared__ float red[T * 16], part[T], gs[2][2 * T];
     __shared__ __attribute__((aligned(16))) float pw[2 * T], pb[2 * T];
     const Slab s = slab_of(a);
@@ -115,8 +116,8 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
     const long long first = (long long)s.n * a.hw;
     Oct<E> raw[NV], draw[NV];
     {
-        const Pixels<E, VEC> x(a.x, a, a.ld_x, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
-        const Pixels<E, VEC> dy(a.dy, a, a.ld_dy, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
+        const Pixels<E, WHOLE> x(a.x, a, a.ld_x, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
+        const Pixels<E, WHOLE> dy(a.dy, a, a.ld_dy, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (p.active && p.pl + i * p.tp < a.hw) {
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_grad_slab_ker
         c1.v[e] *= r.v[e] * r.v[e];
         c2.v[e] *= r.v[e];
     }
-    const Pixels<E, VEC> dx(a.y, a, a.ld_y, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
+    const Pixels<E, WHOLE> dx(a.y, a, a.ld_y, first + p.pl, p.tp, s.c0 + p.vec * 8, valid);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -225,7 +226,7 @@ __device__ __forceinline__ Channels<false> all_channels(const Place &p, const Sl
     return ch;
 }
 
-template <int T, int TYPE>
+template <int T, int TYPE, bool WHOLE>
 __global__ __launch_bounds__(T) void gn_grad_sums_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
@@ -236,8 +237,8 @@ __global__ __launch_bounds__(T) void gn_grad_sums_kernel(GnArgs a)
     float s1[8] = {}, s2[8] = {};
     if (p.active) {
         const long long first = (long long)s.n * a.hw, stat = (long long)s.n * a.groups;
-        Pixels<E, false> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
-        Pixels<E, false> dy(a.dy, a, a.ld_dy, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+        Pixels<E, WHOLE> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+        Pixels<E, WHOLE> dy(a.dy, a, a.ld_dy, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
         const Channels<false> ch = all_channels(p, s, a, stat);
         with_act(a.act, [&](auto act) __attribute__((always_inline)) {
             constexpr int AHEAD = T == 1024 ? 2 : 4;  // pixels in flight
@@ -319,7 +320,7 @@ __device__ __forceinline__ void join_sums(const GnArgs &a, int n, float *g1, flo
     __syncthreads();
 }
 
-template <int T, int TYPE>
+template <int T, int TYPE, bool WHOLE>
 __global__ __launch_bounds__(T) void gn_grad_apply_kernel(GnArgs a)
 {
     typedef typename Elem<TYPE>::type E;
@@ -329,9 +330,9 @@ __global__ __launch_bounds__(T) void gn_grad_apply_kernel(GnArgs a)
     const Place p = place<T>((a.c + 7) / 8);
     const int valid = a.c - p.vec * 8;
     const long long first = (long long)s.n * a.hw, stat = (long long)s.n * a.groups;
-    Pixels<E, false> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
-    Pixels<E, false> dy(a.dy, a, a.ld_dy, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
-    Pixels<E, false> dx(a.y, a, a.ld_y, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, WHOLE> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, WHOLE> dy(a.dy, a, a.ld_dy, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, WHOLE> dx(a.y, a, a.ld_y, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     Oct<E> raw[AHEAD], draw[AHEAD];
     auto request = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
@@ -398,25 +399,35 @@ __global__ __launch_bounds__(1024) void gn_grad_join_kernel(const float *ws, int
     }
 }
 
-template <int T, int NV, bool VEC>
+template <int T, int NV, Mode MODE>
 GnKernel grad_slab_kernel(int type)
 {
-    if constexpr (NV <= (VEC ? 4 : 2))
-        if (type == 0) return gn_grad_slab_kernel<T, NV, 0, VEC>;
-    return type == 1 ? gn_grad_slab_kernel<T, NV, 1, VEC> : gn_grad_slab_kernel<T, NV, 2, VEC>;
+    if constexpr (NV <= (MODE == kVec ? 4 : 2))
+        if (type == 0) return gn_grad_slab_kernel<T, NV, 0, MODE>;
+    return type == 1 ? gn_grad_slab_kernel<T, NV, 1, MODE> : gn_grad_slab_kernel<T, NV, 2, MODE>;
 }
 
-template <bool VEC>
+template <Mode MODE>
 GnKernel grad_slab_kernel_of(const Plan &p, int type)
 {
-    if (p.threads == 256) return p.nv == 2 ? grad_slab_kernel<256, 2, VEC>(type) : grad_slab_kernel<256, 4, VEC>(type);
-    if constexpr (VEC) {
-        if (p.threads == 1024) return grad_slab_kernel<1024, 8, VEC>(type);
-        if (p.nv == 8) return grad_slab_kernel<512, 8, VEC>(type);
+    if (p.threads == 256) return p.nv == 2 ? grad_slab_kernel<256, 2, MODE>(type) : grad_slab_kernel<256, 4, MODE>(type);
+    if constexpr (MODE == kVec) {
+        if (p.nv == 8) return grad_slab_kernel<512, 8, MODE>(type);
     } else if (p.threads == 1024) {
-        return gn_grad_slab_kernel<1024, 2, 0, VEC>;  // float: 16-bit types have {512, 4}
+        return gn_grad_slab_kernel<1024, 2, 0, MODE>;  // float: 16-bit types have {512, 4}
     }
-    return grad_slab_kernel<512, 4, VEC>(type);
+    return grad_slab_kernel<512, 4, MODE>(type);
+}
+
+template <int T, bool WHOLE>
+GnKernel grad_sums_of(const GnArgs &a)
+{
+    return IFX_GN_TYPES(gn_grad_sums_kernel, T, WHOLE);
+}
+template <int T, bool WHOLE>
+GnKernel grad_apply_of(const GnArgs &a)
+{
+    return IFX_GN_TYPES(gn_grad_apply_kernel, T, WHOLE);
 }
 
 }  // namespace
@@ -428,14 +439,19 @@ hipError_t launch_group_norm_grad(GnArgs a, float *dweight, float *dbias, hipStr
     const dim3 block((unsigned)p.threads);
     const int rows = p.nv ? a.n : a.n * p.chunks;
     if (rows > 0 && p.nv) {
-        GnKernel f = a.cg % 8 == 0 ? grad_slab_kernel_of<true>(p, a.type) : grad_slab_kernel_of<false>(p, a.type);
+        const Mode mode = mode_of(p.gs * a.cg, a.cg);
+        GnKernel f = mode == kVec     ? grad_slab_kernel_of<kVec>(p, a.type)
+                     : mode == kWhole ? grad_slab_kernel_of<kWhole>(p, a.type)
+                                      : grad_slab_kernel_of<kRagged>(p, a.type);
         hipLaunchKernelGGL(f, dim3((unsigned)a.per_xcd * 8u), block, 0, s, a);
     } else if (rows > 0) {
         const dim3 grid((unsigned)rows);
         a.gsum = a.ws + (size_t)rows * a.c * 2;
-        const bool small = p.threads == 512;
-        GnKernel sums = small ? IFX_GN_TYPES(gn_grad_sums_kernel, 512) : IFX_GN_TYPES(gn_grad_sums_kernel, 1024);
-        GnKernel apply = small ? IFX_GN_TYPES(gn_grad_apply_kernel, 512) : IFX_GN_TYPES(gn_grad_apply_kernel, 1024);
+        const bool wide = p.threads == 1024, whole = a.c % 8 == 0;
+        GnKernel sums = wide ? (whole ? grad_sums_of<1024, true>(a) : grad_sums_of<1024, false>(a))
+                             : (whole ? grad_sums_of<512, true>(a) : grad_sums_of<512, false>(a));
+        GnKernel apply = wide ? (whole ? grad_apply_of<1024, true>(a) : grad_apply_of<1024, false>(a))
+                              : (whole ? grad_apply_of<512, true>(a) : grad_apply_of<512, false>(a));
         hipLaunchKernelGGL(sums, grid, block, 0, s, a);
         hipLaunchKernelGGL(apply, grid, block, 0, s, a);
     }
