@@ -459,8 +459,9 @@ def fold_bn(x_scale: float, y_scale: float, eps: float, w_scale: torch.Tensor, g
 # ---------------------------------------------------------------------------
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
-# The raw handle of a device's current stream, without a torch.cuda.Stream object around it (these calls are
-# a few microseconds long).
+# The raw handle of a device's current stream, without a torch.cuda.Stream object around it, and the current
+# device (these calls are a few microseconds long).
+_current_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -480,7 +481,7 @@ def _on_device(*ts) -> int:
             raise ValueError(f"tensors of one GPU expected, not {sorted({str(t.device) for t in ts if t is not None})}")
     if index < 0:
         raise ValueError("tensors of a GPU expected")
-    if index != torch.cuda.current_device():
+    if index != _current_index():
         raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{torch.cuda.current_device()}")
     return index
 
@@ -515,14 +516,21 @@ def _pitch(t: torch.Tensor):
     return rows, k, max(ld, k)
 
 
-def _alloc(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+def _alloc(like: torch.Tensor, stream, dtype, *shape) -> torch.Tensor:
     """Uninitialised memory on the device of `like` that belongs to the stream that will use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(*shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+
+
+def _alloc_like(x: torch.Tensor, stream) -> torch.Tensor:
+    """_alloc of x's type and shape, contiguous."""
+    if stream is None and x.is_contiguous():
+        return torch.empty_like(x)
+    return _alloc(x, stream, x.dtype, *x.shape)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -548,7 +556,7 @@ class Mx4(NamedTuple):
 
 def _mx4_like(rows: int, k: int, like: torch.Tensor, stream) -> Mx4:
     k1 = (k + 127) // 128
-    return Mx4(_alloc((k1, rows, 64), torch.uint8, like, stream), _alloc((k1, rows, 4), torch.uint8, like, stream), k)
+    return Mx4(_alloc(like, stream, torch.uint8, k1, rows, 64), _alloc(like, stream, torch.uint8, k1, rows, 4), k)
 
 
 def mx4_empty(rows: int, k: int, device="cuda") -> Mx4:
@@ -592,7 +600,7 @@ def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16, out: Optional[to
     rows, k = _mx4_check(q, "q"), q.k
     ld = k
     if out is None:
-        out = _alloc((rows, k), dtype, q.codes, stream)
+        out = _alloc(q.codes, stream, dtype, rows, k)
     else:
         if out.shape != (rows, k):
             raise ValueError(f"out of shape {tuple(out.shape)}, q of {rows} x {k}")
@@ -614,7 +622,7 @@ def mx4_matmul(a: Mx4, w: Mx4, bias: Optional[torch.Tensor] = None, residual: Op
     _param(bias, n, "bias")
     ld_y = ld_res = n
     if out is None:
-        out = _alloc((m, n), dtype, a.codes, stream)
+        out = _alloc(a.codes, stream, dtype, m, n)
     else:
         if out.shape != (m, n):
             raise ValueError(f"out of shape ({m}, {n}) expected")
@@ -643,7 +651,7 @@ def _gn_desc(x: torch.Tensor, groups: int, act: int, eps: float) -> GnDesc:
 def _gn_ws(d: GnDesc, backward: int, like: torch.Tensor, stream):
     """The workspace (None where none is needed) and its bytes."""
     nbytes = lib().ifx_group_norm_workspace_bytes(d, backward)
-    return (_alloc((nbytes,), torch.uint8, like, stream) if nbytes else None), nbytes
+    return (_alloc(like, stream, torch.uint8, nbytes) if nbytes else None), nbytes
 
 
 def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
@@ -662,12 +670,12 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     _param(weight, d.c, "weight")
     _param(bias, d.c, "bias")
     if out is None:
-        out = _alloc(x.shape, x.dtype, x, stream)
+        out = _alloc_like(x, stream)
         d.ld_y = d.c
     else:
         d.ld_y = _like(out, x, "out")
-    shape = (d.n, max(groups, 0))
-    mean, rstd = _alloc(shape, torch.float32, x, stream), _alloc(shape, torch.float32, x, stream)
+    count = max(groups, 0)  # refused below
+    mean, rstd = _alloc(x, stream, torch.float32, d.n, count), _alloc(x, stream, torch.float32, d.n, count)
     ws, nbytes = _gn_ws(d, 0, x, stream)
     _check(lib().ifx_group_norm(d, x.data_ptr(), _addr(weight), _addr(bias), out.data_ptr(), mean.data_ptr(),
                                 rstd.data_ptr(), _addr(ws), nbytes, _raw_stream(stream, index)), "ifx_group_norm")
@@ -709,11 +717,11 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
             raise ValueError(f"{name}: contiguous float32 of shape ({d.n}, {groups}) expected")
     d.ld_dy = _like(dy, x, "dy")
     if out is None:
-        out = _alloc(x.shape, x.dtype, x, stream)
+        out = _alloc_like(x, stream)
         d.ld_y = d.c
     else:
         d.ld_y = _like(out, x, "out")
-    dweight, dbias = _alloc((d.c,), torch.float32, x, stream), _alloc((d.c,), torch.float32, x, stream)
+    dweight, dbias = _alloc(x, stream, torch.float32, d.c), _alloc(x, stream, torch.float32, d.c)
     ws, nbytes = _gn_ws(d, 1, x, stream)
     _check(lib().ifx_group_norm_backward(d, dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _addr(weight),
                                          _addr(bias), out.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), _addr(ws),

@@ -103,6 +103,20 @@ inline hipError_t current_cus(int *cus)
     return e;
 }
 
+// The compute units a rule may count on, asked of the runtime once a thread and device (256 without one).
+inline int cus_or_default()
+{
+    thread_local int known_dev = -1, known = 256;
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 256;
+    if (dev != known_dev) {
+        if (current_cus(&cus) != hipSuccess) return 256;
+        known = cus;
+        known_dev = dev;
+    }
+    return known;
+}
+
 // Magic multiplier and shift for q = floor(n / d), 0 <= n < 2^31, d >= 1:
 // with p = 31 + ceil(log2 d) and m = ceil(2^p / d), floor(n * m / 2^p) = floor(n / d)
 // (the classic round-up method for dividing by an invariant integer; m < 2^32).

@@ -218,8 +218,7 @@ hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s)
     // The few-rows form reads the weights once a group of 64 rows, a tile of 64 rows costs the same from
     // 1 row to 64 (us, few rows / tiles, weights from HBM): 1 x 8192 x 8192 9.8 / 17.9, 32 rows 13.9 / 18.0,
     // 64 rows 21.9 / 18.2; 64 x 4096 x 4096, one workgroup a CU, 7.2 / 8.8; 64 x 1000 x 2048 5.0 / 5.8.
-    int cus = 0;
-    if (current_cus(&cus) != hipSuccess) cus = 256;
+    const int cus = cus_or_default();
     if (a.m > 64 || (a.m > 32 && a.n > 16 * cus)) return launch_mx4_tiles(a, s);
     if (a.m <= 16)
         launch_rows<1>(a, s);

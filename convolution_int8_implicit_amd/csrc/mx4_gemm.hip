@@ -194,6 +194,7 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
         constexpr bool STEADY = decltype(steady)::value != 0;
         const int8_t *st = smem + slot * C::STAGE;
         int sa[C::FM], sb[C::FN];
+        __builtin_amdgcn_s_setprio(1);
         each(Int<MF>(), [&](auto tt) __attribute__((always_inline)) {
             constexpr int t = decltype(tt)::value, i = t / C::FN, j = t % C::FN;
             if (j == 0) sa[i] = (int)((unsigned)as[i] >> (8 * g));
@@ -205,6 +206,7 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
             if (STEADY) issue_some(s + C::ST - 1, Int<t * C::LPS / MF>(), Int<(t + 1) * C::LPS / MF>());
             __builtin_amdgcn_sched_barrier(0);
         });
+        __builtin_amdgcn_s_setprio(0);
         slot = slot + 1 == C::ST ? 0 : slot + 1;
         const bool more = STEADY || s + 1 < k1;
         if (more) {
@@ -317,8 +319,7 @@ long long tiles(const Mx4Args &a)
 
 hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s)
 {
-    int cus = 0;
-    if (current_cus(&cus) != hipSuccess) cus = 256;
+    const int cus = cus_or_default();
     // The largest tile that gives every CU one (256 CUs; us, large / middle / small tile):
     //   8192 x 2048 x 256 (512 large tiles)    12.4 / 14.4 / 16.8
     //   4096 x 2048 x 2048 (256 large)         17.4 / 18.1 / 21.6

@@ -459,8 +459,7 @@ GnKernel apply_kernel_of(const GnArgs &a, bool mx4, Mode mode)
 Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
 {
     const int cg = c / groups, bytes = type == 0 ? 4 : 2;
-    int cus = 0;
-    if (current_cus(&cus) != hipSuccess) cus = 256;
+    const int cus = cus_or_default();
     // registers for raw values: 64 of a thread's 128, half where a channel's group takes registers of its own
     int most = (type == 0 ? 8 : 16) / (grad ? 2 : 1);
     if (cg % 8 && (type != 0 || grad)) most /= 2;
