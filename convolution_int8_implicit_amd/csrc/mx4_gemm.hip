@@ -294,10 +294,12 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     }
 }
 
-// Three tiles, two of the larger ones' workgroups on a CU (one's epilogue behind the other's steps).
+// Two of the larger tiles' workgroups fit a CU (one's epilogue behind the other's steps), eight of the last's,
+// which is for sums of one or two steps whose residual has to arrive as well.
 typedef Tile<256, 128, 4, 2, 3> TileL;
 typedef Tile<128, 128, 4, 2, 3> TileM;
 typedef Tile<64, 64, 2, 2, 4> TileS;
+typedef Tile<64, 64, 2, 2, 2> TileR;
 
 template <typename C>
 hipError_t launch(const Mx4Args &a, hipStream_t s)
@@ -325,6 +327,9 @@ hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s)
     //   4096 x 2048 x 2048 (256 large)         17.4 / 18.1 / 21.6
     //   2048 x 2048 x 2048 (256 middle)        13.7 / 11.1 / 12.8
     //   1024 x 2048 x 2048 (128 middle)        12.5 /  9.9 /  8.5
+    // and with a residual (bf16, operands from HBM; us, large tile / TileR):
+    //   50176 x 512 x 128   36.4 / 27.7      65536 x 512 x 256   47.4 / 44.5      32768 x 2048 x 512   92 / 103
+    if (a.res && a.k1 <= 2) return launch<TileR>(a, s);
     if (tiles<TileL>(a) >= cus) return launch<TileL>(a, s);
     if (tiles<TileM>(a) >= cus) return launch<TileM>(a, s);
     return launch<TileS>(a, s);
