@@ -1373,6 +1373,8 @@ ifx_status ifx_mx4_matmul(const ifx_mx4_desc *d, const uint8_t *a_codes, const u
     ifx_status st = check_mx4(d->m, d->k);
     if (st == IFX_OK) st = check_mx4(d->n, d->k);
     if (st != IFX_OK) return st;
+    // the grid of the smallest tiles
+    if ((d->m + 63LL) / 64 * ((d->n + 63LL) / 64) > 0xffffffffLL / 256 - 8) return IFX_E_SHAPE;
     if (!pitch_ok(d->m, d->n, d->ld_y) || (residual && !pitch_ok(d->m, d->n, d->ld_res))) return IFX_E_SHAPE;
     if (d->m == 0 || d->n == 0) return IFX_OK;
     if (!y) return IFX_E_NULL;

@@ -25,7 +25,8 @@ __device__ __forceinline__ v8i wide(v4i x) { return (v8i){x[0], x[1], x[2], x[3]
 // Rounding.  Streaming, HBM-bound: a thread rounds eight consecutive columns (one 16-byte load of
 // a 16-bit type), four threads a block, sixteen a row's 128-column panel, so a workgroup covers
 // 16 rows of a panel: 64-byte codes of 16 consecutive rows are a contiguous kilobyte of the
-// output.  Four panels per workgroup keep four loads in flight per thread.
+// output.  Four panels per workgroup keep four loads in flight per thread.  200704 x 512 bf16: 50-57 us
+// and back 44 us for 260 MB either way, 4.6-5.2 and 5.9 TB/s.
 // ------------------------------------------------------------------------------------------
 constexpr int kQRows = 16, kQPanels = 4;
 
@@ -219,7 +220,7 @@ hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s)
     // 1 row to 64 (us, few rows / tiles, weights from HBM): 1 x 8192 x 8192 9.8 / 17.9, 32 rows 13.9 / 18.0,
     // 64 rows 21.9 / 18.2; 64 x 4096 x 4096, one workgroup a CU, 7.2 / 8.8; 64 x 1000 x 2048 5.0 / 5.8.
     const int cus = cus_or_default();
-    if (a.m > 64 || (a.m > 32 && a.n > 16 * cus)) return launch_mx4_tiles(a, s);
+    if (a.m > 64 || (a.m > 32 && a.n > 16 * cus) || a.n > (1 << 24)) return launch_mx4_tiles(a, s);  // (the grid)
     if (a.m <= 16)
         launch_rows<1>(a, s);
     else if (a.m <= 32)

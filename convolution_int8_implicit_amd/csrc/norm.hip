@@ -6,9 +6,12 @@
 // holds at once and joins such parts by their means and counts, as do threads and chunks.
 //
 // What bounds it: memory (each value read and written once in the slab form), closely followed by the
-// vector units: about 20 operations a value with SiLU, whose exponential and reciprocal cost four
-// each.  Hence the activation chosen outside the loops, and z as one fused multiply-add of a
-// 16-bit x, whose own rounding is far coarser than the product's.
+// vector units: about 18 operations a value with SiLU, whose exponential and reciprocal cost four
+// each.  Hence the activation chosen outside the loops, z as one fused multiply-add of a 16-bit x, whose own
+// rounding is far coarser than the product's, and addresses by uniform strides.  bf16 with SiLU: 128 x 784 x 512
+// 41 us, 4.9-5.2 TB/s of the 5.2 that a copy reaches; 128 x 3136 x 256, one slab of 1024 threads a CU so that loads,
+// sums and stores take turns, 107-110 us, 3.7 TB/s; the 4-bit form of the former 39 us, vector-bound.  Split form:
+// 1 x 16384 x 512 20 us.
 #include <algorithm>
 #include <iterator>
 

@@ -3,7 +3,9 @@
 // One sum over the pixels serves everything: with S1[ch] = sum dz xhat and S2[ch] = sum dz, dweight and
 // dbias are their sums over the samples, and a group's sums of d xhat and d are those of weight S1 and
 // weight S2 over its channels.  What bounds it: three passes of memory (x, dy, dx) in the slab form,
-// and the vector units (about 40 operations a value with SiLU).
+// and the vector units (about 40 operations a value with SiLU: dz is computed twice, since keeping it would take
+// the registers that hold the slab).  64 x 784 x 512 bf16 with SiLU 42 us, 3.6 TB/s (no activation 32), and 3 us
+// for dweight and dbias; split form 1 x 16384 x 512 34 us.
 #include "norm_common.h"
 
 namespace ifx {

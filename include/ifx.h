@@ -508,7 +508,7 @@ ifx_status ifx_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32
  *             elements, element-aligned, or NULL; may be y itself (same pitch)
  *   y         DEVICE, m rows of n elements of `type`, one every ld_y >= n
  *             elements, element-aligned; no other operand may overlap it
- *   m, n      >= 0 (either 0: nothing to do); k >= 1
+ *   m, n      >= 0 (either 0: nothing to do), at most 2^24 - 9 tiles of 64 x 64; k >= 1
  * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN,
  * IFX_E_UNSUPPORTED (type, act).
  */

@@ -109,6 +109,18 @@ def test_sizes_and_refusals_need_no_device():
     assert mm(m=0, a=None, y=None) == 0 and mm(n=0, ld_y=0, ld_res=0, w=None) == 0
 
 
+def test_a_grid_past_the_launch_limit_is_refused():
+    """2^32 - 1 work-items: 64 x 64 tiles of 256 threads, with room for the deal over eight XCDs."""
+    L = ifx.lib()
+    fake = ctypes.c_void_p(0x100000)
+
+    def mm(m, n):
+        d = ifx.Mx4Desc(m, n, 64, 1, 0, n, n)
+        return L.ifx_mx4_matmul(ctypes.byref(d), fake, fake, fake, fake, None, None, None, None)
+    assert mm(1 << 18, 1 << 17) == 1          # 2^23 tiles: goes on to the NULL y
+    assert mm(1 << 18, 1 << 18) == 2 and mm(1 << 27, 1 << 10) == 2
+
+
 def test_binding_refusals_need_no_device():
     x = torch.zeros(4, 32)
     with pytest.raises(ValueError):
