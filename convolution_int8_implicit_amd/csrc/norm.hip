@@ -474,6 +474,9 @@ Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
         // a last span of 4-bit codes is padded to whole panels
         const int tcv = (cs + 7) / 8 + (mx4 ? (c + 127) / 128 * 16 - (c + 7) / 8 : 0);
         if ((long long)n * (groups / gs) > (1 << 20)) break;  // the grid
+        // spans of 16 bytes only while their workgroups run at once: the gradient of 32 x 3136 x 256, four a CU,
+        // takes 78 us in them and 69 in the split form, of 128 samples 244 and 228, of 2 samples 16 and 22
+        if (least < 32 && gs * cg * bytes < 32 && (long long)n * (groups / gs) > 2 * cus) break;
         const bool enough = n == 0 || (long long)n * (groups / gs) >= cus;
         if (best.nv && ((least < 64 && best.spans * (long long)n >= cus) || best.gs == gs)) break;
         const Variant *v = grad ? std::begin(kGradSlab) : std::begin(kSlab);
