@@ -5,9 +5,9 @@
 // a wave for 131072 operations; measured alone on operands that change: 6.5 POP/s at 2 waves per
 // SIMD, the 16x16x128 form 5.7), at short sums (k of a few hundred) the output's bytes.  The matrix units'
 // rate follows the chip's power: on zeros they reach 9.9 POP/s at 2.37 GHz, on changing codes 6.5 at 1.67 GHz,
-// with this kernel's LDS reads beside them 5.9.  8192^3 to bf16 takes 268-279 us, 3.9-4.1 POP/s, at 1.64 GHz
-// with the units busy 60 % of the time; 4096^3 41 us; 100352 x 128 x 512 15 us; 2048 x 1000 x 2048, launch and
-// latency, 8.3.
+// with this kernel's LDS reads beside them 5.9.  8192^3 to bf16 takes 250-261 us, 4.2-4.4 POP/s, at 1.6 GHz
+// with the units busy about 60 % of the time; 4096 x 16384 x 16384 483 us, 4.6; 100352 x 128 x 512 15 us;
+// 2048 x 1000 x 2048, launch and latency, 8.3.
 //
 // A workgroup computes a BM x BN tile in steps of one 128-column panel.  A step's operands, BM + BN
 // rows of 64 code bytes and 4 scale bytes, are contiguous runs that buffer->LDS DMA brings into a ring of ST
@@ -298,8 +298,10 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     }
 }
 
-// Two of the larger tiles' workgroups fit a CU (one's epilogue behind the other's steps), eight of the last's,
+// TileX moves the fewest bytes to LDS a product, but has a CU to itself and pays its epilogue in full: for long
+// sums.  Two of TileL's or TileM's workgroups fit a CU (one's epilogue behind the other's steps), eight of TileR's,
 // which is for sums of one or two steps whose residual has to arrive as well.
+typedef Tile<256, 256, 4, 2, 3> TileX;
 typedef Tile<256, 128, 4, 2, 3> TileL;
 typedef Tile<128, 128, 4, 2, 3> TileM;
 typedef Tile<64, 64, 2, 2, 4> TileS;
@@ -334,6 +336,9 @@ hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s)
     // and with a residual (bf16, operands from HBM; us, large tile / TileR):
     //   50176 x 512 x 128   36.4 / 27.7      65536 x 512 x 256   47.4 / 44.5      32768 x 2048 x 512   92 / 103
     if (a.res && a.k1 <= 2) return launch<TileR>(a, s);
+    // and for long sums (us, TileX / large tile):
+    //   8192 x 8192 x 8192   261 / 280       4096 x 4096 x 4096   39.7 / 41.7     8192 x 8192 x 2048   102 / 89
+    if (a.k1 >= 32 && tiles<TileX>(a) >= cus) return launch<TileX>(a, s);
     if (tiles<TileL>(a) >= cus) return launch<TileL>(a, s);
     if (tiles<TileM>(a) >= cus) return launch<TileM>(a, s);
     return launch<TileS>(a, s);

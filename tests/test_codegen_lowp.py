@@ -48,7 +48,7 @@ def test_no_barrier_with_lds_reads_in_flight(assembly, src):
 
 
 @pytest.mark.parametrize("src,kernel,per_cu", [
-    ("mx4_gemm.hip", "TileILi256ELi128", 2), ("mx4_gemm.hip", "TileILi128ELi128", 2), ("mx4_gemm.hip", "TileILi64ELi64", 4),
+    ("mx4_gemm.hip", "TileILi256ELi256", 1), ("mx4_gemm.hip", "TileILi256ELi128", 2), ("mx4_gemm.hip", "TileILi128ELi128", 2), ("mx4_gemm.hip", "TileILi64ELi64", 4),
     ("norm.hip", "gn_slab_kernelILi512", 2), ("norm_grad.hip", "gn_grad_slab_kernelILi512", 2),
     ("norm.hip", "gn_slab_kernelILi1024", 1), ("norm_grad.hip", "gn_grad_slab_kernelILi1024", 1),
 ])

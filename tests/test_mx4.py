@@ -301,6 +301,20 @@ def test_matmul(m, n, k):
 
 
 @pytest.mark.gpu
+def test_matmul_long_sums():
+    """The tile for long sums: every step of the ring many times over, ragged edges; rows and columns sampled."""
+    m, n, k = 4100, 4090, 4200
+    note(f"product {m} x {n} x {k}")
+    a, w, bias, res = product_case(m, n, k, 77)
+    rows = np.unique(np.r_[0:3, 255:258, 2047:2050, m - 5:m, np.random.default_rng(2).integers(0, m, 40)])
+    some = tuple(np.ascontiguousarray(t[:, rows]) for t in a)
+    for kind, act in (("f32", 0), ("bf16", 1)):
+        r = torch.from_numpy(res).to(TYPES[kind])
+        y = ifx.mx4_matmul(tensor_of(a, k), tensor_of(w, k), torch.from_numpy(bias).cuda(), r.cuda(), act, TYPES[kind])
+        check_product(y[torch.from_numpy(rows).cuda()], len(rows), n, k, some, w, bias, f64(r)[rows], act, kind)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_matmul_nan_blocks_and_extreme_scales(m):
     """A NaN scale spoils its row or column alone; scales of 0 and 252 multiply exactly."""
