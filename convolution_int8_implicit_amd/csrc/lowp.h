@@ -64,14 +64,15 @@ struct Words<4> {
     typedef unsigned type __attribute__((ext_vector_type(4), aligned(4)));
 };
 
-template <typename E>
+// ONCE: read once and by one access a line, kept out of the caches that reused data is in.
+template <bool ONCE = false, typename E>
 __device__ __forceinline__ Oct<E> load8(const E *p)
 {
     typedef typename Words<sizeof(E)>::type V;
     Oct<E> o;
 #pragma unroll
     for (int i = 0; i < Oct<E>::W / 4; ++i) {
-        const V v = ((const V *)p)[i];
+        const V v = ONCE ? __builtin_nontemporal_load((const V *)p + i) : ((const V *)p)[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o.w[4 * i + j] = v[j];
     }
@@ -79,10 +80,10 @@ __device__ __forceinline__ Oct<E> load8(const E *p)
 }
 
 // The first `valid` >= 1 of eight values; those past them are arbitrary (the last one again).
-template <typename E>
+template <bool ONCE = false, typename E>
 __device__ __forceinline__ Oct<E> load8(const E *p, int valid)
 {
-    if (valid >= 8) return load8(p);
+    if (valid >= 8) return load8<ONCE>(p);
     Oct<E> o;
     if constexpr (sizeof(E) == 4) {
 #pragma unroll

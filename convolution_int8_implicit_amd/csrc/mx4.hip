@@ -25,12 +25,16 @@ __device__ __forceinline__ v8i wide(v4i x) { return (v8i){x[0], x[1], x[2], x[3]
 // Rounding.  Streaming, HBM-bound: a thread rounds eight consecutive columns (one 16-byte load of
 // a 16-bit type), four threads a block, sixteen a row's 128-column panel, so a workgroup covers
 // 16 rows of a panel: 64-byte codes of 16 consecutive rows are a contiguous kilobyte of the
-// output.  Four panels per workgroup keep four loads in flight per thread.  200704 x 512 bf16: 50-57 us
-// and back 44 us for 260 MB either way, 4.6-5.2 and 5.9 TB/s.
+// output.  Four panels per workgroup keep four loads in flight per thread.  200704 x 512 bf16: 43 us
+// and back 45-48 us for 260 MB either way, 6.0 and 5.4-5.8 TB/s.
+// ONCE: x is read past the caches.  For 16-bit rows that begin on 128-byte lines, where a wave's accesses cover
+// whole lines: the above takes 43 us instead of 47, and with the values back 86 instead of 104, as the codes
+// stay cached.  Elsewhere neighbouring accesses share lines: 100000 x 999 bf16 takes 49 us cached and 52 past the
+// caches, float32 of 1000 columns, two accesses a line, 91 and 108.
 // ------------------------------------------------------------------------------------------
 constexpr int kQRows = 16, kQPanels = 4;
 
-template <int TYPE>
+template <int TYPE, bool ONCE>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *x, long long ld, int rows, int k, int k1,
                                                            int groups, uint8_t *codes, uint8_t *scales)
 {
@@ -44,7 +48,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *x, long l
 #pragma unroll
     for (int i = 0; i < kQPanels; ++i) {
         const int col = (pg * kQPanels + i) * 128 + v * 8;
-        raw[i] = col < k ? load8(src + col, k - col) : Oct<E>{};
+        raw[i] = col < k ? load8<ONCE>(src + col, k - col) : Oct<E>{};
     }
 #pragma unroll
     for (int i = 0; i < kQPanels; ++i) {
@@ -199,7 +203,10 @@ hipError_t launch_mx4_quantize(const void *x, int type, long long ld, int rows, 
 {
     const int k1 = (k + 127) / 128, groups = (k1 + kQPanels - 1) / kQPanels;
     const dim3 grid((unsigned)((rows + kQRows - 1LL) / kQRows * groups));
-    auto *f = type == 0 ? mx4_quantize_kernel<0> : type == 1 ? mx4_quantize_kernel<1> : mx4_quantize_kernel<2>;
+    const bool once = ld % 64 == 0 && ((uintptr_t)x & 127) == 0;
+    auto *f = type == 0   ? mx4_quantize_kernel<0, false>
+              : type == 1 ? (once ? mx4_quantize_kernel<1, true> : mx4_quantize_kernel<1, false>)
+                          : (once ? mx4_quantize_kernel<2, true> : mx4_quantize_kernel<2, false>);
     hipLaunchKernelGGL(f, grid, dim3(256), 0, s, x, ld, rows, k, k1, groups, codes, scales);
     return hipGetLastError();
 }
