@@ -165,7 +165,19 @@ struct Mx4Args {
     int m, n, k1;
     int type, act;
     long long ld_y, ld_res;
+    int past;  // set by the launcher: y is stored past the caches (stored_past)
 };
+
+// Whether rows of a result are stored past the caches: they begin on 128-byte lines, so that stores fill whole
+// lines, and there are more bytes than would stay in the L2s (4 MB in each of eight) until they are read.
+// us, cached / past: product 100352 x 128 x 512 15.1 / 11.8, 50176 x 512 x 128 17.3 / 15.3, 4096^3 38.9 / 37.3;
+// 4-bit values of 200704 x 512 48 / 38, but of 100000 rows of 1000 bf16, which share lines, 62 / 74; a
+// group norm's split form, 4 x 12544 x 1024 forward 70 / 58, its gradient 120 / 110, of 128 x 3136 x 256 228 / 208
+// (its one-read forms were slower past the caches, 51 / 54 for 128 x 784 x 512, and keep to them).
+inline bool stored_past(const void *y, long long rows, long long ld, int bytes)
+{
+    return ld * bytes % 128 == 0 && (reinterpret_cast<uintptr_t>(y) & 127u) == 0 && rows * ld * bytes > (16 << 20);
+}
 
 // One group norm or its gradient (device pointers; see ifx_group_norm).
 struct GnArgs {
@@ -179,8 +191,9 @@ struct GnArgs {
     int type, act;
     float eps;
     long long ld_x, ld_dy, ld_y;
-    // set by the launcher: channels of a group and their division, lanes that sum one group,
-    // chunks of a sample and their pixels
+    // set by the launcher: results stored past the caches (stored_past), channels of a group and their
+    // division, lanes that sum one group, chunks of a sample and their pixels
+    int past;
     int cg, cg_shr;
     unsigned cg_mul;
     int lpg, chunks, px;
@@ -215,7 +228,7 @@ hipError_t launch_mx4_quantize(const void *x, int type, long long ld, int rows, 
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int k, void *y, int type,
                                  long long ld, hipStream_t s);
 hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s);
-hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s);  // its tiled form, mx4_gemm.hip
+hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s);  // its tiled form, mx4_gemm.hip
 // group norm with an activation and its gradient, norm.hip
 bool gn_supported(int n, int hw, int c, int groups);
 size_t gn_workspace_bytes(int n, int hw, int c, int groups, int type, bool grad, bool mx4);

@@ -105,7 +105,12 @@ __device__ __forceinline__ unsigned pack2(float a, float b)
     return __builtin_bit_cast(unsigned, v);
 }
 
-template <typename E>
+// Before and after a store past the caches in one of two branches: without them the compiler joins the two
+// stores into one and drops the mark.
+__device__ __forceinline__ void keep_apart() { asm volatile("" ::: "memory"); }
+
+// PAST: past the caches, for 16-bit results too large to stay there whose rows fill whole lines.
+template <bool PAST = false, typename E>
 __device__ __forceinline__ void store8(E *p, const float (&f)[8])
 {
     typedef typename Words<sizeof(E)>::type V;
@@ -113,7 +118,11 @@ __device__ __forceinline__ void store8(E *p, const float (&f)[8])
         ((V *)p)[0] = (V){__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
         ((V *)p)[1] = (V){__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
     } else {
-        *(V *)p = (V){pack2<E>(f[0], f[1]), pack2<E>(f[2], f[3]), pack2<E>(f[4], f[5]), pack2<E>(f[6], f[7])};
+        const V v = {pack2<E>(f[0], f[1]), pack2<E>(f[2], f[3]), pack2<E>(f[4], f[5]), pack2<E>(f[6], f[7])};
+        if (PAST)
+            __builtin_nontemporal_store(v, (V *)p);
+        else
+            *(V *)p = v;
     }
 }
 

@@ -26,9 +26,9 @@ __device__ __forceinline__ v8i wide(v4i x) { return (v8i){x[0], x[1], x[2], x[3]
 // a 16-bit type), four threads a block, sixteen a row's 128-column panel, so a workgroup covers
 // 16 rows of a panel: 64-byte codes of 16 consecutive rows are a contiguous kilobyte of the
 // output.  Four panels per workgroup keep four loads in flight per thread.  200704 x 512 bf16: 43 us
-// and back 45-48 us for 260 MB either way, 6.0 and 5.4-5.8 TB/s.
+// and back 38 us for 260 MB either way, 6.0 and 6.8 TB/s.
 // ONCE: x is read past the caches.  For 16-bit rows that begin on 128-byte lines, where a wave's accesses cover
-// whole lines: the above takes 43 us instead of 47, and with the values back 86 instead of 104, as the codes
+// whole lines: the above takes 43 us instead of 47, and with the values back 81 instead of 104, as the codes
 // stay cached.  Elsewhere neighbouring accesses share lines: 100000 x 999 bf16 takes 49 us cached and 52 past the
 // caches, float32 of 1000 columns, two accesses a line, 91 and 108.
 // ------------------------------------------------------------------------------------------
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *x, long l
 // type out.  Every value of a finite block is exact in bfloat16.
 template <int TYPE>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *codes, const uint8_t *scales, int rows,
-                                                             int k, int k1, int groups, void *y, long long ld)
+                                                             int k, int k1, int groups, void *y, long long ld, int past)
 {
     typedef typename Elem<TYPE>::type E;
     const int rt = (int)(blockIdx.x / (unsigned)groups), pg = (int)(blockIdx.x - (unsigned)rt * (unsigned)groups);
@@ -101,7 +101,11 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *code
         auto d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sf, 2);
         auto e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sf, 3);
         f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1], f[4] = d[0], f[5] = d[1], f[6] = e[0], f[7] = e[1];
-        store8((E *)y + (long long)row * ld + col, k - col, f);
+        E *const dst = (E *)y + (long long)row * ld + col;
+        if (past && k - col >= 8)
+            store8<true>(dst, f);
+        else
+            store8(dst, k - col, f);
     }
 }
 
@@ -217,7 +221,8 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
     const int k1 = (k + 127) / 128, groups = (k1 + kQPanels - 1) / kQPanels;
     const dim3 grid((unsigned)((rows + kQRows - 1LL) / kQRows * groups));
     auto *f = type == 0 ? mx4_dequantize_kernel<0> : type == 1 ? mx4_dequantize_kernel<1> : mx4_dequantize_kernel<2>;
-    hipLaunchKernelGGL(f, grid, dim3(256), 0, s, codes, scales, rows, k, k1, groups, y, ld);
+    const int past = stored_past(y, rows, ld, type == 0 ? 4 : 2);
+    hipLaunchKernelGGL(f, grid, dim3(256), 0, s, codes, scales, rows, k, k1, groups, y, ld, past);
     return hipGetLastError();
 }
 

@@ -279,7 +279,17 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
                     if (a.res) v += (float)res[p].v[e];
                     q.v[e] = (E)act_of<ACT>(v);
                 }
-                if (whole && row0 + p * RPP < a.m) *(Quad<E> *)((E *)a.y + (row0 + p * RPP) * a.ld_y + col) = q;
+                if (whole && row0 + p * RPP < a.m) {
+                    E *const dst = (E *)a.y + (row0 + p * RPP) * a.ld_y + col;
+                    typedef unsigned Words __attribute__((ext_vector_type(sizeof(E)), aligned(sizeof(E))));
+                    if (a.past) {
+                        keep_apart();
+                        __builtin_nontemporal_store(__builtin_bit_cast(Words, q), (Words *)dst);
+                        keep_apart();
+                    } else {
+                        *(Quad<E> *)dst = q;
+                    }
+                }
             }
             if (left > 0 && !whole) {  // the last one to three columns of y, value by value
 #pragma unroll 1
@@ -325,8 +335,9 @@ long long tiles(const Mx4Args &a)
 
 }  // namespace
 
-hipError_t launch_mx4_tiles(const Mx4Args &a, hipStream_t s)
+hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s)
 {
+    a.past = stored_past(a.y, a.m, a.ld_y, a.type == 0 ? 4 : 2);
     const int cus = cus_or_default();
     // The largest tile that gives every CU one (256 CUs; us, large / middle / small tile):
     //   8192 x 2048 x 256 (512 large tiles)    12.4 / 14.4 / 16.8

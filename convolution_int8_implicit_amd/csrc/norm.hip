@@ -60,8 +60,8 @@ struct Results {
     uint8_t *scale;   // of the block, or null in three threads of four
     int step, valid;
 
-    __device__ __forceinline__ Results(const GnArgs &a, long long row, int step_, int ch, int valid_)
-        : y(a.y, a, a.ld_y, row, step_, ch, valid_), step(step_), valid(valid_)
+    __device__ __forceinline__ Results(const GnArgs &a, long long row, int step_, int ch, int valid_, bool past = false)
+        : y(a.y, a, a.ld_y, row, step_, ch, valid_, past), step(step_), valid(valid_)
     {
         if (MX4) {
             const int vec = ch >> 3;
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
     m.set(p, s, a, [&](int g) { return smean[g]; });
     r.set(p, s, a, [&](int g) { return srstd[g]; });
     f.set(m, r);
-    Results<TYPE, MX4, WHOLE> y(a, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Results<TYPE, MX4, WHOLE> y(a, first + s.p0 + p.pl, p.tp, p.vec * 8, valid, a.past);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
         constexpr int ACT = decltype(act)::value;
         f.template scale<ACT>();
@@ -536,6 +536,7 @@ hipError_t launch_group_norm(GnArgs a, hipStream_t s)
     }
     const dim3 grid((unsigned)(a.n * p.chunks));
     const bool wide = p.threads == 1024;
+    a.past = !mx4 && stored_past(a.y, (long long)a.n * a.hw, a.ld_y, a.type == 0 ? 4 : 2);
     GnKernel stats = wide ? stats_kernel_of<1024>(a, mode) : stats_kernel_of<512>(a, mode);
     GnKernel apply = wide ? apply_kernel_of<1024>(a, mx4, mode) : apply_kernel_of<512>(a, mx4, mode);
     hipLaunchKernelGGL(stats, grid, block, 0, s, a);

@@ -105,9 +105,11 @@ struct Pixels {
     const E *at, *end;
     long long stride;
     int valid;
-    __device__ __forceinline__ Pixels(const void *p, const GnArgs &a, long long ld, long long row, int step, int ch, int valid_)
+    bool past;  // stored past the caches
+    __device__ __forceinline__ Pixels(const void *p, const GnArgs &a, long long ld, long long row, int step, int ch, int valid_,
+                                      bool past_ = false)
         : at((const E *)p + row * ld + ch), end((const E *)p + ((long long)a.n * a.hw - 1) * ld + a.c), stride(step * ld),
-          valid(valid_)
+          valid(valid_), past(past_)
     {
     }
     __device__ __forceinline__ Oct<E> get(int i) const
@@ -121,10 +123,15 @@ struct Pixels {
     __device__ __forceinline__ void put(int i, const float (&f)[8]) const
     {
         E *p = const_cast<E *>(at) + i * stride;
-        if constexpr (WHOLE)
-            store8(p, f);
-        else
+        if constexpr (!WHOLE) {
             store8(p, valid, f);
+        } else if (past) {
+            keep_apart();
+            store8<true>(p, f);
+            keep_apart();
+        } else {
+            store8(p, f);
+        }
     }
     // on by i steps
     __device__ __forceinline__ void advance(int i) { at += i * stride; }

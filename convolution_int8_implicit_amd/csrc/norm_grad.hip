@@ -334,7 +334,7 @@ __global__ __launch_bounds__(T) void gn_grad_apply_kernel(GnArgs a)
     const long long first = (long long)s.n * a.hw, stat = (long long)s.n * a.groups;
     Pixels<E, WHOLE> x(a.x, a, a.ld_x, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
     Pixels<E, WHOLE> dy(a.dy, a, a.ld_dy, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
-    Pixels<E, WHOLE> dx(a.y, a, a.ld_y, first + s.p0 + p.pl, p.tp, p.vec * 8, valid);
+    Pixels<E, WHOLE> dx(a.y, a, a.ld_y, first + s.p0 + p.pl, p.tp, p.vec * 8, valid, a.past);
     Oct<E> raw[AHEAD], draw[AHEAD];
     auto request = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
@@ -450,6 +450,7 @@ hipError_t launch_group_norm_grad(GnArgs a, float *dweight, float *dbias, hipStr
         const dim3 grid((unsigned)rows);
         a.gsum = a.ws + (size_t)rows * a.c * 2;
         const bool wide = p.threads == 1024, whole = a.c % 8 == 0;
+        a.past = stored_past(a.y, (long long)a.n * a.hw, a.ld_y, a.type == 0 ? 4 : 2);
         GnKernel sums = wide ? (whole ? grad_sums_of<1024, true>(a) : grad_sums_of<1024, false>(a))
                              : (whole ? grad_sums_of<512, true>(a) : grad_sums_of<512, false>(a));
         GnKernel apply = wide ? (whole ? grad_apply_of<1024, true>(a) : grad_apply_of<1024, false>(a))

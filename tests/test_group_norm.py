@@ -215,6 +215,22 @@ def test_backward(n, hw, c, groups):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("pitch", [64, 72])
+def test_results_larger_than_the_caches(pitch):
+    """Two samples of 70000 pixels, 18 MB of bf16, in rows that fill 128-byte lines and rows that share them."""
+    n, hw, c, groups = 2, 70000, 64, 8
+    x, dy, w, b = case(n, hw, c, "bf16", 91)
+    wd, bd = w.cuda(), b.cuda()
+    y, dx = (torch.full((n, hw, pitch), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    note(f"group_norm {n}x{hw}x{c} pitch {pitch}")
+    _, mean, rstd = ifx.group_norm(x.cuda(), groups, wd, bd, 1e-5, ifx.ACT_SILU, out=y[:, :, :c])
+    _, dw, db = ifx.group_norm_backward(dy.cuda(), x.cuda(), mean, rstd, groups, wd, bd, ifx.ACT_SILU, out=dx[:, :, :c])
+    check_forward(x, groups, w, b, 1e-5, ifx.ACT_SILU, y[:, :, :c], mean, rstd, "bf16")
+    check_backward(dy, x, mean, rstd, groups, w, b, ifx.ACT_SILU, dx[:, :, :c], dw, db, "bf16")
+    assert bool((y[:, :, c:] == 7).all()) and bool((dx[:, :, c:] == 7).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", [0, 1, 2])
 def test_gradient_against_differences(act):
     """The kernel's gradient along a direction against the difference of the 64-bit forward pass; off by

@@ -362,6 +362,33 @@ def test_matmul_pitches_in_place_and_stream(m, n, off):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("pitch", [128, 136])
+def test_results_larger_than_the_caches(pitch):
+    """Results of 18 MB and more in rows that fill 128-byte lines and rows that share them, their last columns and
+    last rows inside a tile."""
+    m, n, k = 70001, 125, 64
+    a, w, bias, res = product_case(m, n, k, 11)
+    A, W = tensor_of(a, k), tensor_of(w, k)
+    for kind, with_res in (("bf16", False), ("f16", True), ("f32", True)):
+        note(f"product {m} x {n} x {k} {kind}, rows of {pitch}")
+        wq = (w[0], w[1] - 7 * (w[1] > 0).astype(np.uint8))  # keeps float16 results finite
+        r = torch.from_numpy(res * 0.01).to(TYPES[kind]) if with_res else None
+        wide = torch.full((m, pitch), 3.0, dtype=TYPES[kind], device="cuda")
+        ifx.mx4_matmul(A, tensor_of(wq, k), torch.from_numpy(bias).cuda(), None if r is None else r.cuda(),
+                       ifx.ACT_RELU, out=wide[:, :n])
+        check_product(wide[:, :n], m, n, k, a, wq, bias, None if r is None else f64(r), ifx.ACT_RELU, kind)
+        assert bool((wide[:, n:] == 3).all())
+    codes, scales = product_case(m, 2, 117, 12)[0]
+    v = lowp.mx4_values(codes, scales, 117)
+    for kind in ("bf16", "f16", "f32"):
+        note(f"values {m} x 117 {kind}, rows of {pitch}")
+        wide = torch.full((m, pitch), 3.0, dtype=TYPES[kind], device="cuda")
+        ifx.mx4_dequantize(tensor_of((codes, scales), 117), out=wide[:, :117])
+        assert np.array_equal(f64(wide[:, :117]), v.astype(np.float16).astype(np.float64) if kind == "f16" else v)
+        assert bool((wide[:, 117:] == 3).all())
+
+
+@pytest.mark.gpu
 def test_matmul_same_from_call_to_call_and_in_a_graph():
     m, n, k = 130, 200, 1024
     a, w, bias, _ = product_case(m, n, k, 9)
