@@ -170,7 +170,7 @@ struct Mx4Args {
 
 // Whether rows of a result are stored past the caches: they begin on 128-byte lines, so that stores fill whole
 // lines, and there are more bytes than would stay in the L2s (4 MB in each of eight) until they are read.
-// us, cached / past: product 100352 x 128 x 512 15.1 / 11.8, 50176 x 512 x 128 17.3 / 15.3, 4096^3 38.9 / 37.3;
+// us, cached / past: product 100352 x 128 x 512 14.9 / 11.8, 50176 x 512 x 128 17.2 / 15.5, 4096^3 39.8 / 37.7;
 // 4-bit values of 200704 x 512 48 / 38, but of 100000 rows of 1000 bf16, which share lines, 62 / 74; a
 // group norm's split form, 4 x 12544 x 1024 forward 70 / 58, its gradient 120 / 110, of 128 x 3136 x 256 228 / 208
 // (its one-read forms were slower past the caches, 51 / 54 for 128 x 784 x 512, and keep to them).

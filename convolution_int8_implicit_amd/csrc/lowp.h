@@ -107,7 +107,7 @@ __device__ __forceinline__ unsigned pack2(float a, float b)
 
 // Before and after a store past the caches in one of two branches: without them the compiler joins the two
 // stores into one and drops the mark.
-__device__ __forceinline__ void keep_apart() { asm volatile("" ::: "memory"); }
+__device__ __forceinline__ void keep_apart() { asm volatile(""); }
 
 // PAST: past the caches, for 16-bit results too large to stay there whose rows fill whole lines.
 template <bool PAST = false, typename E>

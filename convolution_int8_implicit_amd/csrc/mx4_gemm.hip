@@ -73,6 +73,9 @@ struct Tile {
     static constexpr int LPS = CA + CB + SPW;                 // DMAs per wave and stage
     static constexpr int ROW = TN * 4 + 32;         // bytes of a staged output row: 4 rows apart, half the banks on
     static constexpr int OUT = 32 * ROW * W;
+    // whether large results go past the caches: TileS gets small ones, and with a second copy of its epilogue
+    // 2048 x 1000 x 2048 took 9.0 us instead of 8.8
+    static constexpr bool PAST = BM * BN > 64 * 64 || ST == 2;
     static constexpr int LDS = ST * STAGE > OUT ? ST * STAGE : OUT;
     static constexpr int PER_CU = kLdsBytes / LDS < 2048 / T ? kLdsBytes / LDS : 2048 / T;
     static_assert(BM % (16 * W) == 0 && BN % (16 * W) == 0, "every wave brings as much of A and of W");
@@ -269,28 +272,32 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
         wave_lds_sync();
         with_act(a.act, [&](auto act) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act)::value;
+            auto rows = [&](auto past) __attribute__((always_inline)) {
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const v4f f = *(const v4f *)(out + (p * RPP + el / LPR) * C::ROW + (el % LPR) * 16);
-                Quad<E> q;
+                for (int p = 0; p < P; ++p) {
+                    const v4f f = *(const v4f *)(out + (p * RPP + el / LPR) * C::ROW + (el % LPR) * 16);
+                    Quad<E> q;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = f[e] + bias[e];
-                    if (a.res) v += (float)res[p].v[e];
-                    q.v[e] = (E)act_of<ACT>(v);
-                }
-                if (whole && row0 + p * RPP < a.m) {
+                    for (int e = 0; e < 4; ++e) {
+                        float v = f[e] + bias[e];
+                        if (a.res) v += (float)res[p].v[e];
+                        q.v[e] = (E)act_of<ACT>(v);
+                    }
+                    if (!whole || row0 + p * RPP >= a.m) continue;
                     E *const dst = (E *)a.y + (row0 + p * RPP) * a.ld_y + col;
-                    typedef unsigned Words __attribute__((ext_vector_type(sizeof(E)), aligned(sizeof(E))));
-                    if (a.past) {
-                        keep_apart();
+                    if constexpr (decltype(past)::value) {
+                        typedef unsigned Words __attribute__((ext_vector_type(sizeof(E)), aligned(sizeof(E))));
                         __builtin_nontemporal_store(__builtin_bit_cast(Words, q), (Words *)dst);
                         keep_apart();
                     } else {
                         *(Quad<E> *)dst = q;
                     }
                 }
-            }
+            };
+            if (C::PAST && a.past)
+                rows(std::true_type());
+            else
+                rows(std::false_type());
             if (left > 0 && !whole) {  // the last one to three columns of y, value by value
 #pragma unroll 1
                 for (int k = 0; k < P * left; ++k) {
