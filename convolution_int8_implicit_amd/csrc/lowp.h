@@ -105,8 +105,8 @@ __device__ __forceinline__ unsigned pack2(float a, float b)
     return __builtin_bit_cast(unsigned, v);
 }
 
-// Before and after a store past the caches in one of two branches: without them the compiler joins the two
-// stores into one and drops the mark.
+// Beside a store past the caches in one of two branches: without it the compiler joins the two branches' stores
+// into one and drops the mark.
 __device__ __forceinline__ void keep_apart() { asm volatile(""); }
 
 // PAST: past the caches, for 16-bit results too large to stay there whose rows fill whole lines.
