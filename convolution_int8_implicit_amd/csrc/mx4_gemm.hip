@@ -352,7 +352,8 @@ hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s)
     //   2048 x 2048 x 2048 (256 middle)        13.7 / 11.1 / 12.8
     //   1024 x 2048 x 2048 (128 middle)        12.5 /  9.9 /  8.5
     // and with a residual (bf16, operands from HBM; us, large tile / TileR):
-    //   50176 x 512 x 128   36.4 / 27.7      65536 x 512 x 256   47.4 / 44.5      32768 x 2048 x 512   92 / 103
+    //   50176 x 512 x 128   34.9 / 29.0      200704 x 256 x 64   64.0 / 51.4      65536 x 512 x 256   45.5 / 43.7
+    //   32768 x 2048 x 256  81.5 / 85.6 (the one loss seen)     32768 x 2048 x 512    92 / 103 (so not for longer)
     if (a.res && a.k1 <= 2) return launch<TileR>(a, s);
     // and for long sums (us, TileX / large tile):
     //   8192 x 8192 x 8192   261 / 280       4096 x 4096 x 4096   39.7 / 41.7     8192 x 8192 x 2048   102 / 89
