@@ -31,7 +31,7 @@ __all__ = [
     "BLOCK_SCRATCH_BYTES", "net_workspace_bytes",
     "net_forward", "NetGraph", "fold_bn", "BnFold", "status_string", "last_hip_error", "version", "LIB_PATH",
     "ACT_NONE", "ACT_RELU", "ACT_SILU", "Mx4", "mx4_empty", "mx4_quantize", "mx4_dequantize", "mx4_matmul",
-    "group_norm", "group_norm_mx4", "group_norm_backward",
+    "group_norm", "group_norm_mx4", "group_norm_backward", "GnDesc", "group_norm_kernel_name",
 ]
 
 RELU, RESIDUAL, MAXPOOL, OUT_I32, INPUT_NHWC, OUT_EVEN, OUT_PHASE, IN_PHASE = 1, 2, 4, 8, 16, 32, 64, 128
@@ -143,6 +143,7 @@ def lib() -> ctypes.CDLL:
         "ifx_group_norm": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
         "ifx_group_norm_mx4": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
         "ifx_group_norm_backward": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "ifx_group_norm_kernel_name": ([ctypes.POINTER(GnDesc), i32, ctypes.c_char_p, sz], i32),
         "ifx_status_string": ([i32], ctypes.c_char_p),
         "ifx_probe_copy": ([vp, vp, sz, vp], i32),
         "ifx_probe_mfma_i8": ([vp, i32, i32, vp], i32),
@@ -658,6 +659,14 @@ def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
     if t.shape != x.shape or t.dtype != x.dtype:
         raise ValueError(f"{name}: shape {tuple(x.shape)} and {x.dtype} expected")
     return _pitch(t)[2]
+
+
+def group_norm_kernel_name(d: GnDesc, form: int = 0) -> str:
+    """The (first) kernel instance that ifx_group_norm (form 0), its gradient (1) or its 4-bit form (2) launches
+    for d, as profilers print it (host-only query)."""
+    buf = ctypes.create_string_buffer(256)
+    _check(lib().ifx_group_norm_kernel_name(ctypes.byref(d), form, buf, len(buf)), "ifx_group_norm_kernel_name")
+    return buf.value.decode()
 
 
 def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,

@@ -1458,4 +1458,20 @@ ifx_status ifx_group_norm_backward(const ifx_gn_desc *d, const void *dy, const v
     return hip_status(ifx::launch_group_norm_grad(a, dweight, dbias, (hipStream_t)stream));
 }
 
+ifx_status ifx_group_norm_kernel_name(const ifx_gn_desc *d, int32_t form, char *buf, size_t len)
+{
+    if (form < 0 || form > 2) return IFX_E_UNSUPPORTED;
+    ifx_status st = check_gn(d, form == 1, form == 2);
+    if (st != IFX_OK) return st;
+    if (d->n == 0) return IFX_E_SHAPE;
+    if (!buf) return IFX_E_NULL;
+    uint8_t some;
+    ifx::GnArgs a = gn_args(d, nullptr, nullptr, nullptr, nullptr);
+    if (form == 2) a.codes = &some;  // asks for the 4-bit form; nothing is launched
+    ArmedQuery aq;
+    st = hip_status(form == 1 ? ifx::launch_group_norm_grad(a, nullptr, nullptr, nullptr) : ifx::launch_group_norm(a, nullptr));
+    if (st != IFX_OK) return st;
+    return copy_name(aq.q, buf, len);
+}
+
 }  // extern "C"

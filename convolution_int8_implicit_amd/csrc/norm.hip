@@ -384,6 +384,7 @@ int sum_lanes(int groups, int threads)
 Plan plan_split(int n, int hw, int c, int groups)
 {
     Plan p = {};
+    p.slab = -1;
     p.threads = c <= 2048 ? 512 : 1024;
     const int tp = p.threads / ((c + 7) / 8);
     int most = (hw + kBatch * tp - 1) / (kBatch * tp);
@@ -400,39 +401,17 @@ Plan plan_split(int n, int hw, int c, int groups)
     return p;
 }
 
-// The threads and vectors per thread of the slab kernels, by rising capacity.
-struct Variant {
-    int threads, nv;
-};
-constexpr Variant kSlab[] = {{256, 2}, {256, 8}, {512, 8}, {512, 16}, {1024, 16}};
-constexpr Variant kGradSlab[] = {{256, 2}, {256, 4}, {512, 4}, {1024, 2}, {512, 8}};
-
-template <int T, int NV, bool MX4, Mode MODE>
-GnKernel slab_kernel(int type)
+// Entry `at` of kSlab.
+template <int TYPE, bool MX4, Mode MODE, int I = 0>
+Instance slab_entry(int at)
 {
-    if constexpr (NV <= 8)
-        if (type == 0) return gn_slab_kernel<T, NV, 0, MX4, MODE>;
-    return type == 1 ? gn_slab_kernel<T, NV, 1, MX4, MODE> : gn_slab_kernel<T, NV, 2, MX4, MODE>;
-}
-
-template <bool MX4, Mode MODE>
-GnKernel slab_kernel_of(const Plan &p, int type)
-{
-    if (p.threads == 256)
-        return p.nv == 2 ? slab_kernel<256, 2, MX4, MODE>(type) : slab_kernel<256, 8, MX4, MODE>(type);
-    if constexpr (MODE == kVec) {
-        if (p.threads == 1024) return slab_kernel<1024, 16, MX4, MODE>(type);
-        if (p.nv == 16) return slab_kernel<512, 16, MX4, MODE>(type);
+    if constexpr (I < (int)std::size(kSlab)) {
+        if (at != I) return slab_entry<TYPE, MX4, MODE, I + 1>(at);
+        constexpr Variant v = kSlab[I];
+        if constexpr (slab_holds(v, TYPE, MODE == kVec, false))
+            return {gn_slab_kernel<v.threads, v.nv, TYPE, MX4, MODE>, v.threads, v.nv};
     }
-    return slab_kernel<512, 8, MX4, MODE>(type);
-}
-
-template <bool MX4>
-GnKernel slab_kernel_of(const Plan &p, int type, Mode mode)
-{
-    return mode == kVec     ? slab_kernel_of<MX4, kVec>(p, type)
-           : mode == kWhole ? slab_kernel_of<MX4, kWhole>(p, type)
-                            : slab_kernel_of<MX4, kRagged>(p, type);
+    return {};
 }
 
 template <int T>
@@ -463,10 +442,8 @@ Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
 {
     const int cg = c / groups, bytes = type == 0 ? 4 : 2;
     const int cus = cus_or_default();
-    // registers for raw values: 64 of a thread's 128, half where a channel's group takes registers of its own
-    int most = (type == 0 ? 8 : 16) / (grad ? 2 : 1);
-    if (cg % 8 && (type != 0 || grad)) most /= 2;
     Plan best = {};
+    best.slab = -1;
     for (int least = 128; least >= 16; least /= 2) {
         int gs = 1;
         while (gs < groups && (groups % gs || gs * cg * bytes < least || (mx4 && gs * cg % 32))) ++gs;
@@ -478,20 +455,21 @@ Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
         // takes 78 us in them and 69 in the split form, of 128 samples 244 and 228, of 2 samples 16 and 22
         if (least < 32 && gs * cg * bytes < 32 && (long long)n * (groups / gs) > 2 * cus) break;
         const bool enough = n == 0 || (long long)n * (groups / gs) >= cus;
-        if (best.nv && ((least < 64 && best.spans * (long long)n >= cus) || best.gs == gs)) break;
+        if (best.slab >= 0 && ((least < 64 && best.spans * (long long)n >= cus) || best.gs == gs)) break;
         const Variant *v = grad ? std::begin(kGradSlab) : std::begin(kSlab);
         const Variant *const end = grad ? std::end(kGradSlab) : std::end(kSlab);
         for (; v != end; ++v)
-            if (v->nv <= most && tcv <= v->threads / 4 && (long long)v->threads / tcv * v->nv >= hw) {
+            if (slab_holds(*v, type, cg % 8 == 0, grad) && tcv <= v->threads / 4 &&
+                (long long)v->threads / tcv * v->nv >= hw) {
                 best.threads = v->threads;
-                best.nv = v->nv;
+                best.slab = (int)(v - (grad ? std::begin(kGradSlab) : std::begin(kSlab)));
                 best.gs = gs;
                 best.spans = groups / gs;
                 break;
             }
-        if (best.nv && enough && (long long)hw * cs <= 32768) break;
+        if (best.slab >= 0 && enough && (long long)hw * cs <= 32768) break;
     }
-    return best.nv ? best : plan_split(n, hw, c, groups);
+    return best.slab >= 0 ? best : plan_split(n, hw, c, groups);
 }
 
 void gn_fill(GnArgs &a, const Plan &p)
@@ -504,13 +482,13 @@ void gn_fill(GnArgs &a, const Plan &p)
     a.gs = p.gs;
     a.spans = p.spans;
     a.per_xcd = (int)(((long long)a.n * p.spans + 7) / 8);
-    a.lpg = sum_lanes(p.nv ? p.gs : a.groups, p.threads);
+    a.lpg = sum_lanes(p.slab >= 0 ? p.gs : a.groups, p.threads);
 }
 
 size_t gn_workspace_bytes(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
 {
     const Plan p = gn_plan(n, hw, c, groups, type, grad, mx4);
-    if (p.nv) return grad ? (size_t)n * 2 * c * 4 : 0;
+    if (p.slab >= 0) return grad ? (size_t)n * 2 * c * 4 : 0;
     const size_t rows = (size_t)n * p.chunks;
     return rows * 4 * 2 * ((size_t)groups + (grad ? (size_t)c : 0));
 }
@@ -527,14 +505,18 @@ hipError_t launch_group_norm(GnArgs a, hipStream_t s)
     const bool mx4 = a.codes != nullptr;
     const Plan p = gn_plan(a.n, a.hw, a.c, a.groups, a.type, false, mx4);
     gn_fill(a, p);
-    const dim3 block((unsigned)p.threads);
-    const Mode mode = mode_of(p.nv ? p.gs * a.cg : a.c, a.cg);
-    if (p.nv) {
-        GnKernel f = mx4 ? slab_kernel_of<true>(p, a.type, mode) : slab_kernel_of<false>(p, a.type, mode);
-        hipLaunchKernelGGL(f, dim3((unsigned)a.per_xcd * 8u), block, 0, s, a);
+    const Mode mode = mode_of(p.slab >= 0 ? p.gs * a.cg : a.c, a.cg);
+    if (p.slab >= 0) {
+        const Instance k = with_type_mode(a.type, mode, [&](auto type, auto m) {
+            return mx4 ? slab_entry<type.value, true, m.value>(p.slab) : slab_entry<type.value, false, m.value>(p.slab);
+        });
+        if (!k.kernel) return hipErrorInvalidDeviceFunction;
+        if (answer_query("gn_slab_kernel<%d, %d, %d, %s, (ifx::Mode)%d>", k.threads, k.nv, a.type, tf(mx4), mode)) return hipSuccess;
+        hipLaunchKernelGGL(k.kernel, dim3((unsigned)a.per_xcd * 8u), dim3((unsigned)k.threads), 0, s, a);
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)(a.n * p.chunks));
+    if (answer_query("gn_stats_kernel<%d, %d, (ifx::Mode)%d>", p.threads, a.type, mode)) return hipSuccess;
+    const dim3 grid((unsigned)(a.n * p.chunks)), block((unsigned)p.threads);
     const bool wide = p.threads == 1024;
     a.past = !mx4 && stored_past(a.y, (long long)a.n * a.hw, a.ld_y, a.type == 0 ? 4 : 2);
     GnKernel stats = wide ? stats_kernel_of<1024>(a, mode) : stats_kernel_of<512>(a, mode);

@@ -16,6 +16,8 @@
 //          parts and reads x again.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "ifx_internal.h"
 #include "lowp.h"
@@ -215,16 +217,53 @@ __device__ __forceinline__ void stage_params(const Slab &s, const GnArgs &a, flo
     }
 }
 
-// Sets up the launcher's fields of `a` for a plan.
+// ------------------------------------------------------------------------------------------
+// Host side
+// ------------------------------------------------------------------------------------------
+typedef void (*GnKernel)(GnArgs);
+
+// The threads and vectors per thread of the slab kernels, by rising capacity.  Plan and dispatch both walk these
+// lists, and an entry is compiled for just the types and modes whose plans may take it (slab_holds).
+struct Variant {
+    int threads, nv;
+};
+constexpr Variant kSlab[] = {{256, 2}, {256, 8}, {512, 8}, {512, 16}, {1024, 16}};
+constexpr Variant kGradSlab[] = {{256, 2}, {256, 4}, {512, 4}, {1024, 2}, {512, 8}};
+
+// Registers for raw values: 64 of a thread's 128 (x and dy in the gradient), half where a channel's group takes
+// registers of its own (vec: it takes none) beside packed values or a second tensor.
+constexpr bool slab_holds(Variant v, int type, bool vec, bool grad)
+{
+    const int most = (type == 0 ? 8 : 16) / (grad ? 2 : 1);
+    return v.nv <= (vec || (type == 0 && !grad) ? most : most / 2);
+}
+
+// A slab kernel and the block it is compiled for; kernel: null where the entry is not compiled.
+struct Instance {
+    GnKernel kernel;
+    int threads, nv;
+};
+
+// f(type, mode) as compile-time constants.
+template <typename F>
+Instance with_type_mode(int type, Mode mode, F f)
+{
+    auto modes = [&](auto t) {
+        return mode == kVec     ? f(t, std::integral_constant<Mode, kVec>())
+               : mode == kWhole ? f(t, std::integral_constant<Mode, kWhole>())
+                                : f(t, std::integral_constant<Mode, kRagged>());
+    };
+    return type == 0 ? modes(Slot0()) : type == 1 ? modes(Slot1()) : modes(Slot2());
+}
+
 struct Plan {
     int threads;
-    int nv, gs, spans;  // slab: vectors per thread, groups of a span, spans; nv = 0: split
-    int chunks, px;     // split: chunks of a sample and their pixels
+    int slab, gs, spans;  // slab: entry of its list, groups of a span, spans; slab = -1: split
+    int chunks, px;       // split: chunks of a sample and their pixels
 };
 Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4);
+// Sets up the launcher's fields of `a` for a plan.
 void gn_fill(GnArgs &a, const Plan &p);
-
-typedef void (*GnKernel)(GnArgs);
 
 #define IFX_GN_TYPES(kernel, T, ...)                                                            \
     (a.type == 0 ? kernel<T, 0, ##__VA_ARGS__> : a.type == 1 ? kernel<T, 1, ##__VA_ARGS__> : kernel<T, 2, ##__VA_ARGS__>)

@@ -6,6 +6,8 @@
 // and the vector units (about 40 operations a value with SiLU: dz is computed twice, since keeping it would take
 // the registers that hold the slab).  64 x 784 x 512 bf16 with SiLU 42 us, 3.6 TB/s (no activation 32), and 3 us
 // for dweight and dbias; split form 1 x 16384 x 512 34 us.
+#include <iterator>
+
 #include "norm_common.h"
 
 namespace ifx {
@@ -401,24 +403,17 @@ __global__ __launch_bounds__(1024) void gn_grad_join_kernel(const float *ws, int
     }
 }
 
-template <int T, int NV, Mode MODE>
-GnKernel grad_slab_kernel(int type)
+// Entry `at` of kGradSlab.
+template <int TYPE, Mode MODE, int I = 0>
+Instance grad_slab_entry(int at)
 {
-    if constexpr (NV <= (MODE == kVec ? 4 : 2))
-        if (type == 0) return gn_grad_slab_kernel<T, NV, 0, MODE>;
-    return type == 1 ? gn_grad_slab_kernel<T, NV, 1, MODE> : gn_grad_slab_kernel<T, NV, 2, MODE>;
-}
-
-template <Mode MODE>
-GnKernel grad_slab_kernel_of(const Plan &p, int type)
-{
-    if (p.threads == 256) return p.nv == 2 ? grad_slab_kernel<256, 2, MODE>(type) : grad_slab_kernel<256, 4, MODE>(type);
-    if constexpr (MODE == kVec) {
-        if (p.nv == 8) return grad_slab_kernel<512, 8, MODE>(type);
-    } else if (p.threads == 1024) {
-        return gn_grad_slab_kernel<1024, 2, 0, MODE>;  // float: 16-bit types have {512, 4}
+    if constexpr (I < (int)std::size(kGradSlab)) {
+        if (at != I) return grad_slab_entry<TYPE, MODE, I + 1>(at);
+        constexpr Variant v = kGradSlab[I];
+        if constexpr (slab_holds(v, TYPE, MODE == kVec, true))
+            return {gn_grad_slab_kernel<v.threads, v.nv, TYPE, MODE>, v.threads, v.nv};
     }
-    return grad_slab_kernel<512, 4, MODE>(type);
+    return {};
 }
 
 template <int T, bool WHOLE>
@@ -438,18 +433,19 @@ hipError_t launch_group_norm_grad(GnArgs a, float *dweight, float *dbias, hipStr
 {
     const Plan p = gn_plan(a.n, a.hw, a.c, a.groups, a.type, true, false);
     gn_fill(a, p);
-    const dim3 block((unsigned)p.threads);
-    const int rows = p.nv ? a.n : a.n * p.chunks;
-    if (rows > 0 && p.nv) {
+    const bool slab = p.slab >= 0;
+    const int rows = slab ? a.n : a.n * p.chunks;
+    if (rows > 0 && slab) {
         const Mode mode = mode_of(p.gs * a.cg, a.cg);
-        GnKernel f = mode == kVec     ? grad_slab_kernel_of<kVec>(p, a.type)
-                     : mode == kWhole ? grad_slab_kernel_of<kWhole>(p, a.type)
-                                      : grad_slab_kernel_of<kRagged>(p, a.type);
-        hipLaunchKernelGGL(f, dim3((unsigned)a.per_xcd * 8u), block, 0, s, a);
+        const Instance k = with_type_mode(a.type, mode, [&](auto type, auto m) { return grad_slab_entry<type.value, m.value>(p.slab); });
+        if (!k.kernel) return hipErrorInvalidDeviceFunction;
+        if (answer_query("gn_grad_slab_kernel<%d, %d, %d, (ifx::Mode)%d>", k.threads, k.nv, a.type, mode)) return hipSuccess;
+        hipLaunchKernelGGL(k.kernel, dim3((unsigned)a.per_xcd * 8u), dim3((unsigned)k.threads), 0, s, a);
     } else if (rows > 0) {
-        const dim3 grid((unsigned)rows);
+        const dim3 grid((unsigned)rows), block((unsigned)p.threads);
         a.gsum = a.ws + (size_t)rows * a.c * 2;
         const bool wide = p.threads == 1024, whole = a.c % 8 == 0;
+        if (answer_query("gn_grad_sums_kernel<%d, %d, %s>", p.threads, a.type, tf(whole))) return hipSuccess;
         a.past = stored_past(a.y, (long long)a.n * a.hw, a.ld_y, a.type == 0 ? 4 : 2);
         GnKernel sums = wide ? (whole ? grad_sums_of<1024, true>(a) : grad_sums_of<1024, false>(a))
                              : (whole ? grad_sums_of<512, true>(a) : grad_sums_of<512, false>(a));

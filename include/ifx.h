@@ -571,6 +571,12 @@ ifx_status ifx_group_norm_backward(const ifx_gn_desc *d, const void *dy, const v
                                    float *dweight, float *dbias, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * Host-only: the (first) kernel instance that ifx_group_norm (form 0), ifx_group_norm_backward (form 1) or
+ * ifx_group_norm_mx4 (form 2) launches for d with n >= 1, as ifx_conv_kernel_name below answers for a convolution.
+ */
+ifx_status ifx_group_norm_kernel_name(const ifx_gn_desc *d, int32_t form, char *buf, size_t len);
+
+/*
  * Host-only: the kernel instance ifx_conv_fused(d, ...) launches, named as
  * profilers print it (e.g. "igemm_kernel<3, 3, 128, 128, 2, false, true,
  * false>"), written NUL-terminated into buf.  The name comes from the very

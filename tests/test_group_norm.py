@@ -13,6 +13,8 @@ e_dz = |dy| (0.55 e_z + (|z| + 8) 2 e) for SiLU, 2 e |dy| otherwise (a ReLU's co
 single 32-bit operations, as here); sums as above on top of their terms' own errors.
 """
 import ctypes
+import random
+import re
 import sys
 
 import numpy as np
@@ -394,3 +396,86 @@ def test_same_from_call_to_call_and_in_a_graph():
         if i < 2:
             for p, q in zip(out, first):
                 assert torch.equal(p, q)
+
+
+# ------------------------------------------------------------------------------------------ dispatch
+
+def slab_of(name):
+    """(gradient, threads, vectors, type, 4-bit, mode) of a slab kernel's name, None of another's."""
+    m = re.match(r"gn_(grad_)?slab_kernel<(\d+), (\d+), (\d+), (?:(true|false), )?\(ifx::Mode\)(\d)>$", name)
+    return m and (m[1] is not None, int(m[2]), int(m[3]), int(m[4]), m[5] == "true", int(m[6]))
+
+
+def check_dispatch(n, hw, c, groups, kind, form):
+    """The instance that a call launches is of its tensors' type and of the mode its groups allow, keeps no more
+    registers of values than the kernels' launch bounds leave, and holds every pixel of one of the spans of whole
+    groups that a sample can be cut into."""
+    d = ifx.GnDesc(n, hw, c, groups, kind, 0, 1e-5, c, c, c)
+    name, cg = ifx.group_norm_kernel_name(d, form), c // groups
+    what = (n, hw, c, groups, kind, form, name)
+    s = slab_of(name)
+    if s is None:
+        m = re.match(r"gn_(stats|grad_sums)_kernel<(\d+), (\d+), ", name)
+        assert m and (m[1] == "grad_sums") == (form == 1) and int(m[3]) == kind, what
+        assert int(m[2]) >= (c + 7) // 8, what
+        return name
+    grad, threads, vectors, of, mx4, mode = s
+    assert of == kind and grad == (form == 1) and mx4 == (form == 2), what
+    assert vectors * (8 if kind == 0 else 4) * (2 if grad else 1) <= 64, what
+    fits = False
+    for gs in (g for g in range(1, groups + 1) if groups % g == 0):
+        cs = gs * cg
+        if mx4 and cs % 32 and gs < groups:
+            continue
+        tcv = (cs + 7) // 8 + ((c + 127) // 128 * 16 - (c + 7) // 8 if mx4 else 0)
+        m = 2 if cg % 8 == 0 else 1 if cs % 8 == 0 else 0
+        fits = fits or (tcv <= threads // 4 and threads // tcv * vectors >= hw and m == mode)
+    assert fits, what
+    return name
+
+
+# (n, hw, c, groups) at the edges of the gradient's slabs: one or a few wide groups over few pixels, spans whose last
+# pixels only the widest workgroup holds
+EDGES = [(8, 8, 2048, 1), (8, 1, 1536, 1), (2, 8, 2048, 1), (1, 18, 876, 1), (1, 8, 2620, 2), (1, 33, 3696, 8), (64, 42, 764, 2),
+         (2, 7, 1036, 1), (40, 41, 1520, 4), (2, 169, 384, 4), (1, 169, 96, 1), (2, 225, 72, 1), (3, 9, 1100, 1), (2, 2, 2047, 1)]
+
+
+def test_every_plan_has_its_kernel():
+    seen = set()
+    rng = random.Random(5)
+    shapes = EDGES + SHAPES + [(1, hw, c, g) for hw in (1, 2, 5, 8, 9, 14, 42, 169, 340, 1024, 2100) for g in (1, 2, 4, 8, 32)
+                               for c in (g, 8 * g, 12 * g, 31 * g, 96 * g, 1032, 1100, 1536, 2048, 8192) if c % g == 0 and c <= 8192]
+    for _ in range(3000):
+        g = rng.choice((1, 2, 4, 8, 12, 32))
+        shapes.append((int(2 ** rng.uniform(0, 9)), int(2 ** rng.uniform(0, 12)), g * max(1, int(2 ** rng.uniform(0, 13)) // g), g))
+    for n, hw, c, groups in shapes:
+        for kind in (0, 1, 2):
+            for form in (0, 1, 2):
+                seen.add(check_dispatch(n, hw, c, groups, kind, form))
+    # the sweep has to reach what the gradient can choose: both kinds of group in the widest workgroup, each type
+    for kind in (0, 1, 2):
+        assert f"gn_grad_slab_kernel<1024, 2, {kind}, (ifx::Mode)2>" in seen
+        assert any(f"gn_grad_slab_kernel<1024, 2, {kind}, (ifx::Mode){m}>" in seen for m in (0, 1))
+
+
+def test_kernel_name_refusals():
+    d = ifx.GnDesc(1, 9, 8, 4, 1, 0, 1e-5, 8, 8, 8)
+    L, buf = ifx.lib(), ctypes.create_string_buffer(256)
+    assert L.ifx_group_norm_kernel_name(ctypes.byref(d), 0, buf, 256) == 0
+    assert L.ifx_group_norm_kernel_name(ctypes.byref(d), 3, buf, 256) == 3 and L.ifx_group_norm_kernel_name(ctypes.byref(d), -1, buf, 256) == 3
+    assert L.ifx_group_norm_kernel_name(None, 0, buf, 256) == 1 and L.ifx_group_norm_kernel_name(ctypes.byref(d), 0, None, 256) == 1
+    assert L.ifx_group_norm_kernel_name(ctypes.byref(d), 0, buf, 4) == 5
+    d.n = 0
+    assert L.ifx_group_norm_kernel_name(ctypes.byref(d), 0, buf, 256) == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,hw,c,groups", EDGES)
+def test_backward_of_wide_groups_over_few_pixels(n, hw, c, groups):
+    note(f"group norm gradient {n} x {hw} x {c}, {groups} groups")
+    for kind, act in (("f32", 2), ("bf16", 2), ("f16", 0), ("bf16", 1)):
+        x, dy, w, b = case(n, hw, c, kind, n + hw + c + groups)
+        _, _, mean, rstd = lowp.group_norm(f64(x), groups, f64(w), f64(b), 1e-5)
+        mean, rstd = torch.from_numpy(mean).float(), torch.from_numpy(rstd).float()
+        dx, dw, db = ifx.group_norm_backward(dy.cuda(), x.cuda(), mean.cuda(), rstd.cuda(), groups, w.cuda(), b.cuda(), act)
+        check_backward(dy, x, mean, rstd, groups, w, b, act, dx, dw, db, kind)
