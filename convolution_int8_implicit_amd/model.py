@@ -18,7 +18,7 @@ DEFAULT_SUB_BATCH = 0
 
 from . import (ACT_NONE, ACT_SILU, INPUT_NHWC, BlockParams, ConvDesc, NetGraph, NetParams, block_forward, block_workspace_bytes,
                conv_desc, conv_fused, conv_out_dims, dequantize_i32, group_norm, group_norm_backward, group_norm_mx4, mx4_matmul,
-               mx4_quantize, net_forward, net_workspace_bytes, pack_act, pack_weights, synth)
+               mx4_quantize, net_forward, net_workspace_bytes, pack_act, pack_weights, synth, _alloc)
 
 
 @dataclass
@@ -156,8 +156,9 @@ class NormPointwise4:
         self.groups, self.scale, self.act, self.out_act, self.eps = groups, scale, act, out_act, eps
 
     def features(self, acc: torch.Tensor, stream=None) -> torch.Tensor:
-        """float32 features of int32 accumulators [n, h, w, c]."""
-        return dequantize_i32(acc, self.scale, stream=stream)
+        """float32 features of int32 accumulators [n, h, w, c], memory of the stream that computes them."""
+        out = _alloc(acc, stream, torch.float32, *acc.shape)
+        return dequantize_i32(acc, self.scale, out=out, stream=stream)
 
     def forward(self, acc: torch.Tensor, residual: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
                 stream=None) -> torch.Tensor:

@@ -85,3 +85,48 @@ def test_layer_in_a_graph_and_its_gradient():
         layer.norm_weight -= 20.0 * dw
         layer.norm_bias -= 20.0 * db
     assert losses[2] < losses[1] < losses[0]
+
+
+def test_features_belong_to_the_stream_that_computes_them(monkeypatch):
+    """The features that forward() drops while its kernels still run are memory of the given stream: another
+    stream's next allocation cannot be given it."""
+    made, used = [], []
+
+    def alloc(like, stream, dtype, *shape):
+        made.append((stream, dtype, shape))
+        return torch.empty(*shape, dtype=dtype)
+
+    def dequantize(q, scale, out=None, stream=None):
+        used.append((out, stream))
+        return torch.empty(q.shape) if out is None else out
+    monkeypatch.setattr(ifx, "_alloc", alloc)
+    monkeypatch.setattr(model, "_alloc", alloc, raising=False)
+    monkeypatch.setattr(model, "dequantize_i32", dequantize)
+    layer = model.NormPointwise4.__new__(model.NormPointwise4)
+    layer.scale = 0.5
+    acc = torch.zeros(2, 3, 4, 32, dtype=torch.int32)
+    x = layer.features(acc, "a stream")
+    assert made == [("a stream", torch.float32, (2, 3, 4, 32))]
+    assert len(used) == 1 and used[0][0] is x and used[0][1] == "a stream"
+
+
+@pytest.mark.gpu
+def test_layer_on_a_given_stream():
+    """The layer on a stream that is still busy, while the current stream allocates and fills memory: the result
+    is that of the calls in order."""
+    layer, acc, *_ = layer_and_input()
+    res = torch.randn(*acc.shape[:-1], 96, device="cuda").to(torch.bfloat16)
+    expect = layer.forward(acc, res)
+    work = torch.zeros(1 << 28, device="cuda")
+    s = torch.cuda.Stream()
+    for given in (s, s.cuda_stream):
+        torch.cuda.synchronize()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(8):
+                work.add_(1.0)
+        y = layer.forward(acc, res, stream=given)
+        fill = [torch.full(acc.shape, float("nan"), device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, expect)
+        del fill
