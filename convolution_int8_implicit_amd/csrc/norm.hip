@@ -6,9 +6,9 @@
 // holds at once and joins such parts by their means and counts, as do threads and chunks.
 //
 // What bounds it: memory (each value read and written once in the slab form), closely followed by the
-// vector units: about 18 operations a value with SiLU, whose exponential and reciprocal cost four
-// each.  Hence the activation chosen outside the loops, z as one fused multiply-add of a 16-bit x, whose own
-// rounding is far coarser than the product's, and addresses by uniform strides.  bf16 with SiLU: 128 x 784 x 512
+// vector units: about 19 operations a value with SiLU, whose exponential and reciprocal cost four
+// each.  Hence the activation chosen outside the loops, z as one subtraction and one fused multiply-add, and addresses by
+// uniform strides.  bf16 with SiLU: 128 x 784 x 512
 // 41 us, 4.9-5.2 TB/s of the 5.2 that a copy reaches; 128 x 3136 x 256, one slab of 1024 threads a CU so that loads,
 // sums and stores take turns, 107-110 us, 3.7 TB/s; the 4-bit form of the former 39 us, vector-bound.  Split form:
 // 1 x 16384 x 512 20 us.
@@ -20,8 +20,10 @@
 namespace ifx {
 namespace {
 
-// A value's z from the group's mean and rstd and the channel's weight and bias.
-template <int TYPE, bool VEC>
+// A value's z from the group's mean and rstd and the channel's weight and bias.  The mean is subtracted first, also
+// from 16-bit values: as x w' + (b - mean w') it would be one operation less, but off by the rounding of mean w', which
+// in a nearly constant group (w' up to weight / sqrt(eps)) is far more than the bias.
+template <bool VEC>
 struct Affine {
     float w[8], b[8];
     PerGroup<VEC> m;
@@ -29,10 +31,7 @@ struct Affine {
     {
         m = mean;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[e] *= rstd.get(e);
-            if (TYPE != 0) b[e] = fmaf(-mean.get(e), w[e], b[e]);
-        }
+        for (int e = 0; e < 8; ++e) w[e] *= rstd.get(e);
     }
     template <int ACT>
     __device__ __forceinline__ void scale()
@@ -45,10 +44,7 @@ struct Affine {
             }
     }
     // pre_scale times it, after scale()
-    __device__ __forceinline__ float z(float x, int e) const
-    {
-        return TYPE == 0 ? fmaf(x - m.get(e), w[e], b[e]) : fmaf(x, w[e], b[e]);
-    }
+    __device__ __forceinline__ float z(float x, int e) const { return fmaf(x - m.get(e), w[e], b[e]); }
 };
 
 // Where a thread's results go: eight channels from channel ch on of pixels row + i * step.
@@ -72,7 +68,7 @@ struct Results {
     }
 
     template <int ACT, bool VEC>
-    __device__ __forceinline__ void put(int i, const Oct<E> &raw, const Affine<TYPE, VEC> &f) const
+    __device__ __forceinline__ void put(int i, const Oct<E> &raw, const Affine<VEC> &f) const
     {
         float v[8];
 #pragma unroll
@@ -172,7 +168,7 @@ __global__ __launch_bounds__(T, T / 256 > 1 ? T / 256 : 1) void gn_slab_kernel(G
         for (int i = threadIdx.x; i < s.ng; i += T)
             a.rstd[(long long)s.n * a.groups + s.g0 + i] = 1.0f / sqrtf(gs[i] / total + a.eps);
     if (!p.active) return;
-    Affine<TYPE, VEC> f;
+    Affine<VEC> f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         f.w[e] = pw[p.vec * 8 + e];
@@ -334,7 +330,7 @@ __global__ __launch_bounds__(T) void gn_apply_kernel(GnArgs a)
     };
     if (T == 1024) join_stats<T>(a, s.n, smean, srstd);  // first here: 128 registers do not hold both
     request(s.p0 + p.pl);
-    Affine<TYPE, false> f;
+    Affine<false> f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int ch = p.vec * 8 + e;

@@ -479,3 +479,54 @@ def test_backward_of_wide_groups_over_few_pixels(n, hw, c, groups):
         mean, rstd = torch.from_numpy(mean).float(), torch.from_numpy(rstd).float()
         dx, dw, db = ifx.group_norm_backward(dy.cuda(), x.cuda(), mean.cuda(), rstd.cuda(), groups, w.cuda(), b.cuda(), act)
         check_backward(dy, x, mean, rstd, groups, w, b, act, dx, dw, db, kind)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c,groups", [(64, 8), (40, 8), (33, 3)])
+@pytest.mark.parametrize("hw", [40, 9000])
+def test_constant_groups_of_large_values(hw, c, groups):
+    """Every pixel of a group the same large value, in each type: the mean is that value (p 2^q of few bits, whose
+    sums are exact as long as their count times p is below 2^24), the variance 0, and y = act(bias), however large
+    rstd and the mean are; its codes are those of act(bias)."""
+    n = 2
+    rng = np.random.default_rng(4)
+    w = torch.from_numpy(1 + 0.5 * rng.standard_normal(c)).float()
+    b = torch.from_numpy(0.5 * rng.standard_normal(c)).float()
+    for kind in ("f32", "bf16", "f16"):
+        for value in (7.0, 1000.0, 57344.0, -57344.0):
+            assert hw * c // groups * 125 < 2 ** 24
+            note(f"group norm, constant {value} {kind}, {n} x {hw} x {c}, {groups} groups")
+            x = torch.full((n, hw, c), value, dtype=TYPES[kind])
+            for act in (0, 1, 2):
+                y, mean, rstd = ifx.group_norm(x.cuda(), groups, w.cuda(), b.cuda(), 1e-5, act)
+                assert (mean == value).all() and np.allclose(f64(rstd), 1e-5 ** -0.5, rtol=1e-6)
+                exact = np.broadcast_to(lowp.act(f64(b), act), (n, hw, c)).copy()
+                tol = (np.abs(f64(b)) + 4) * 4 * E * np.abs(exact) if act == 2 else 0 * exact
+                assert excess(f64(y), exact, tol, kind) == 0
+                if act < 2:
+                    codes, scales = lowp.mx4_quantize(exact[0, :1])
+                    q = ifx.group_norm_mx4(x.cuda(), groups, w.cuda(), b.cuda(), 1e-5, act)
+                    assert (q.codes.cpu().numpy() == codes).all() and (q.scales.cpu().numpy() == scales).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c,groups", [(64, 8), (40, 8), (33, 3)])
+def test_nearly_constant_groups_of_large_values(c, groups):
+    """Two pixels of each group off its large value by the last bit of float16, one up and one down: the mean is the
+    value, exactly, and the bound has no part that grows with it."""
+    n, hw, value = 2, 40, 1024.0
+    cg = c // groups
+    rng = np.random.default_rng(6)
+    w = torch.from_numpy(1 + 0.5 * rng.standard_normal(c)).float()
+    b = torch.from_numpy(0.5 * rng.standard_normal(c)).float()
+    x = torch.full((n, hw, c), value)
+    x[:, 3, ::cg] += 1
+    x[:, 29, cg - 1::cg] -= 1
+    z, xhat, mean, rstd = lowp.group_norm(f64(x), groups, f64(w), f64(b), 1e-5)
+    # (mean exact: forward_bounds with d(mean) = 0 and x - mean, not x, times rstd w)
+    tol = np.abs(f64(w) * xhat) * 40 * E + 4 * E * (np.abs(f64(w) * xhat) + np.abs(f64(b)))
+    for kind in ("f32", "f16"):
+        note(f"group norm, nearly constant {kind}, {n} x {hw} x {c}, {groups} groups")
+        y, m, r = ifx.group_norm(x.to(TYPES[kind]).cuda(), groups, w.cuda(), b.cuda(), 1e-5, 0)
+        assert (m == value).all() and worst(f64(r), rstd, 40 * E * rstd) <= 1
+        assert excess(f64(y), z, tol, kind) == 0
