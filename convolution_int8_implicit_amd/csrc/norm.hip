@@ -240,7 +240,7 @@ __global__ __launch_bounds__(T) void gn_stats_kernel(GnArgs a)
             for (int e = 0; e < P; ++e) {
                 const float d = sum[e] - mean[e];
                 mean[e] = fmaf(d, part, mean[e]);
-                m2[e] += fmaf(d * d, both, sq[e]);
+                m2[e] += fmaf(d, d * both, sq[e]);  // d is the mean itself while nothing is joined: both first, 0 then
             }
             cnt += have;
         }
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(T) void gn_stats_kernel(GnArgs a)
 #pragma unroll
     for (int e = 0; e < P; ++e) {
         const float d = mean[e] - m.get(e);
-        v[e] = fmaf(d * d, each, m2[e]);
+        v[e] = fmaf(d, d * each, m2[e]);
     }
     __syncthreads();
     group_sums<T, VEC>(v, p, s, a, red, gs);
@@ -294,7 +294,7 @@ __device__ __forceinline__ void join_stats(const GnArgs &a, int n, float *smean,
         for (int i = 0; i < kJoin; ++i) {
             const int k = sub + i * a.lpg;
             const float d = t[i].x - mean;
-            f += fmaf(d * d, k < a.chunks - 1 ? full : k == a.chunks - 1 ? rest : 0.0f, t[i].y);
+            f += fmaf(d, d * (k < a.chunks - 1 ? full : k == a.chunks - 1 ? rest : 0.0f), t[i].y);
         }
         const float var = lanes_sum(f, a.lpg) / total;
         if (sub == 0) {

@@ -530,3 +530,21 @@ def test_nearly_constant_groups_of_large_values(c, groups):
         y, m, r = ifx.group_norm(x.to(TYPES[kind]).cuda(), groups, w.cuda(), b.cuda(), 1e-5, 0)
         assert (m == value).all() and worst(f64(r), rstd, 40 * E * rstd) <= 1
         assert excess(f64(y), z, tol, kind) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c,groups", [(64, 8), (33, 3)])
+@pytest.mark.parametrize("hw", [40, 9000])
+def test_means_whose_square_overflows(hw, c, groups):
+    """A mean of 2^67, whose square is past float32: the variance is that of the differences, whose squares are not."""
+    n = 2
+    x, _, w, b = case(n, hw, c, "f32", 12)
+    note(f"group norm, mean 2^67, {n} x {hw} x {c}, {groups} groups")
+    for kind in ("f32", "bf16"):
+        flat = torch.full((n, hw, c), 2.0 ** 67, dtype=TYPES[kind])
+        y, mean, rstd = ifx.group_norm(flat.cuda(), groups, w.cuda(), b.cuda(), 1e-5, 0)
+        assert (mean == 2.0 ** 67).all() and np.allclose(f64(rstd), 1e-5 ** -0.5, rtol=1e-6)
+        assert torch.equal(y.cpu(), b.to(TYPES[kind]).expand(n, hw, c))
+    far = (x.double() * 2.0 ** 54 + 2.0 ** 67).float()
+    y, mean, rstd = ifx.group_norm(far.cuda(), groups, w.cuda(), b.cuda(), 1e-5, 1)
+    check_forward(far, groups, w, b, 1e-5, 1, y, mean, rstd, "f32")
