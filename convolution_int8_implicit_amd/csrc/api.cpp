@@ -1403,10 +1403,11 @@ ifx_status ifx_mx4_matmul(const ifx_mx4_desc *d, const uint8_t *a_codes, const u
 
 size_t ifx_group_norm_workspace_bytes(const ifx_gn_desc *d, int32_t backward)
 {
-    if (check_gn(d, backward != 0, false) != IFX_OK) return 0;
-    const size_t need = ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, d->type, backward != 0, false);
-    if (backward) return need;
-    return std::max(need, ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, d->type, false, true));
+    auto need = [d](bool grad, bool mx4) -> size_t {
+        if (check_gn(d, grad, mx4) != IFX_OK) return 0;
+        return ifx::gn_workspace_bytes(d->n, d->hw, d->c, d->groups, d->type, grad, mx4);
+    };
+    return backward ? need(true, false) : std::max(need(false, false), need(false, true));
 }
 
 ifx_status ifx_group_norm(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias, void *y,

@@ -540,8 +540,8 @@ ifx_status ifx_mx4_matmul(const ifx_mx4_desc *d, const uint8_t *a_codes, const u
  *   dweight = sum over samples and pixels of dz * xhat,  dbias = sum of dz
  * from the forward pass's mean and rstd.  dweight or dbias may be NULL.
  *   x, y, dy, dx  DEVICE, of `type`, element-aligned, pitches ld_x, ld_y (y
- *                 or dx) and ld_dy (the gradient only).  y may be x and dx may
- *                 be x or dy (same pitch)
+ *                 or dx; not looked at by the 4-bit form) and ld_dy (the
+ *                 gradient only).  y may be x and dx may be x or dy (same pitch)
  *   weight, bias  DEVICE float32 [c], 4-byte aligned, or NULL (1 and 0)
  *   dweight, dbias, mean, rstd  DEVICE float32, 4-byte aligned
  *   n >= 0, hw >= 1, 1 <= c <= 8192, groups >= 1 dividing c, eps >= 0
@@ -558,7 +558,10 @@ typedef struct {
     int64_t ld_x, ld_y, ld_dy;
 } ifx_gn_desc;
 
-/* Host-only: workspace bytes of the forward calls (backward 0) or the gradient (1); 0 for a bad desc. */
+/*
+ * Host-only: workspace bytes of the gradient (backward 1) or the larger of the two forward calls' (0; a call
+ * for which d is not valid counts as 0: without ld_y, ifx_group_norm); 0 for a bad desc.
+ */
 size_t ifx_group_norm_workspace_bytes(const ifx_gn_desc *d, int32_t backward);
 
 ifx_status ifx_group_norm(const ifx_gn_desc *d, const void *x, const float *weight, const float *bias, void *y,

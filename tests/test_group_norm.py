@@ -548,3 +548,16 @@ def test_means_whose_square_overflows(hw, c, groups):
     far = (x.double() * 2.0 ** 54 + 2.0 ** 67).float()
     y, mean, rstd = ifx.group_norm(far.cuda(), groups, w.cuda(), b.cuda(), 1e-5, 1)
     check_forward(far, groups, w, b, 1e-5, 1, y, mean, rstd, "f32")
+
+
+def test_workspace_of_the_4_bit_form_needs_no_ld_y():
+    """The 4-bit form has no y: a descriptor without its pitch is valid for it, and so is the query's answer."""
+    L, fake = ifx.lib(), ctypes.c_void_p(0x100000)
+    for n, hw, c, groups in ((3, 100003, 64, 8), (1, 16384, 512, 32), (1, 5000, 33, 3)):
+        full, none = (ifx.GnDesc(n, hw, c, groups, 1, 0, 1e-5, c, ld_y, 0) for ld_y in (c, 0))
+        need = L.ifx_group_norm_workspace_bytes(ctypes.byref(none), 0)
+        assert 0 < need <= L.ifx_group_norm_workspace_bytes(ctypes.byref(full), 0)
+        # far enough to ask for the codes: not IFX_E_WORKSPACE
+        assert L.ifx_group_norm_mx4(ctypes.byref(none), fake, None, None, None, fake, None, None, fake, need, None) == 1
+        assert L.ifx_group_norm(ctypes.byref(none), fake, None, None, fake, None, None, fake, 1 << 40, None) == 2
+    assert L.ifx_group_norm_workspace_bytes(ctypes.byref(ifx.GnDesc(1, 9, 8, 4, 1, 0, 1e-5, 7, 0, 0)), 0) == 0
