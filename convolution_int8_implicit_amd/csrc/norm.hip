@@ -434,10 +434,12 @@ GnKernel apply_kernel_of(const GnArgs &a, bool mx4, Mode mode)
 // the spans are too few to give every CU one (1 x 3136 x 256: 16.7 at 64 bytes, 8.6 at 16; the
 // neighbouring spans of so small a tensor meet in the caches) or 64 does not fit.  A 4-bit result
 // needs spans of whole blocks of 32 columns.
+// The plan also sizes the caller's workspace, before any device is chosen: it counts on the MI355X's compute
+// units and asks no device for its own.
+constexpr int kCus = 256;
 Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
 {
     const int cg = c / groups, bytes = type == 0 ? 4 : 2;
-    const int cus = cus_or_default();
     Plan best = {};
     best.slab = -1;
     for (int least = 128; least >= 16; least /= 2) {
@@ -449,9 +451,9 @@ Plan gn_plan(int n, int hw, int c, int groups, int type, bool grad, bool mx4)
         if ((long long)n * (groups / gs) > (1 << 20)) break;  // the grid
         // spans of 16 bytes only while their workgroups run at once: the gradient of 32 x 3136 x 256, four a CU,
         // takes 78 us in them and 69 in the split form, of 128 samples 244 and 228, of 2 samples 16 and 22
-        if (least < 32 && gs * cg * bytes < 32 && (long long)n * (groups / gs) > 2 * cus) break;
-        const bool enough = n == 0 || (long long)n * (groups / gs) >= cus;
-        if (best.slab >= 0 && ((least < 64 && best.spans * (long long)n >= cus) || best.gs == gs)) break;
+        if (least < 32 && gs * cg * bytes < 32 && (long long)n * (groups / gs) > 2 * kCus) break;
+        const bool enough = n == 0 || (long long)n * (groups / gs) >= kCus;
+        if (best.slab >= 0 && ((least < 64 && best.spans * (long long)n >= kCus) || best.gs == gs)) break;
         const Variant *v = grad ? std::begin(kGradSlab) : std::begin(kSlab);
         const Variant *const end = grad ? std::end(kGradSlab) : std::end(kSlab);
         for (; v != end; ++v)

@@ -13,8 +13,11 @@ e_dz = |dy| (0.55 e_z + (|z| + 8) 2 e) for SiLU, 2 e |dy| otherwise (a ReLU's co
 single 32-bit operations, as here); sums as above on top of their terms' own errors.
 """
 import ctypes
+import os
 import random
 import re
+import shutil
+import subprocess
 import sys
 
 import numpy as np
@@ -561,3 +564,55 @@ def test_workspace_of_the_4_bit_form_needs_no_ld_y():
         assert L.ifx_group_norm_mx4(ctypes.byref(none), fake, None, None, None, fake, None, None, fake, need, None) == 1
         assert L.ifx_group_norm(ctypes.byref(none), fake, None, None, fake, None, None, fake, 1 << 40, None) == 2
     assert L.ifx_group_norm_workspace_bytes(ctypes.byref(ifx.GnDesc(1, 9, 8, 4, 1, 0, 1e-5, 7, 0, 0)), 0) == 0
+
+
+HOST_ONLY = r"""
+#include <dlfcn.h>
+#include <stdio.h>
+#include "ifx.h"
+/* takes the runtime's place: a device of 32 compute units, and a count of who asks */
+static int asked;
+int hipGetDevice(int *dev) { ++asked; *dev = 0; return 0; }
+int hipDeviceGetAttribute(int *v, int attr, int dev) { ++asked; *v = 32; return 0; }
+int hipGetDeviceCount(int *n) { ++asked; *n = 1; return 0; }
+int main(int argc, char **argv)
+{
+    void *l = dlopen(argv[1], RTLD_NOW);
+    if (!l) { puts(dlerror()); return 1; }
+    size_t (*bytes)(const ifx_gn_desc *, int32_t) = (size_t (*)(const ifx_gn_desc *, int32_t))dlsym(l, "ifx_group_norm_workspace_bytes");
+    ifx_status (*norm)(const ifx_gn_desc *, const void *, const float *, const float *, void *, float *, float *, void *, size_t, void *) =
+        (ifx_status (*)(const ifx_gn_desc *, const void *, const float *, const float *, void *, float *, float *, void *, size_t, void *))dlsym(l, "ifx_group_norm");
+    ifx_gn_desc d = {0};
+    int n, hw, c, groups;
+    asked = 0;
+    while (scanf("%d %d %d %d", &n, &hw, &c, &groups) == 4) {
+        d.n = n, d.hw = hw, d.c = c, d.groups = groups, d.type = IFX_BF16, d.ld_x = d.ld_y = d.ld_dy = c;
+        printf("%zu %zu %d\n", bytes(&d, 0), bytes(&d, 1), (int)norm(&d, &d, 0, 0, 0, 0, 0, 0, 0, 0));
+    }
+    printf("asked %d\n", asked);
+    return 0;
+}
+"""
+
+
+def test_validation_touches_no_device(tmp_path):
+    """The workspace query and the checks of a call ask the runtime nothing, so a workspace sized under one device
+    serves any other."""
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not available")
+    src, exe = tmp_path / "host.c", tmp_path / "host"
+    src.write_text(HOST_ONLY)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-rdynamic", "-I", os.path.join(root, "include"), str(src), "-o", str(exe), "-ldl"], check=True)
+    ifx.lib()
+    shapes = SHAPES + [(1, 3136, 256, 32), (32, 3136, 256, 32), (2, 3136, 256, 32), (64, 784, 512, 32)]
+    r = subprocess.run([str(exe), ifx.LIB_PATH], input="\n".join(" ".join(map(str, s)) for s in shapes), capture_output=True, text=True,
+                       timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
+    *lines, asked = r.stdout.split("\n")[:-1]
+    assert asked == "asked 0"
+    for (n, hw, c, groups), line in zip(shapes, lines, strict=True):
+        d = ifx.GnDesc(n, hw, c, groups, 1, 0, 0.0, c, c, c)
+        forward, backward, status = map(int, line.split())
+        assert [forward, backward] == [ifx.lib().ifx_group_norm_workspace_bytes(ctypes.byref(d), i) for i in (0, 1)], (n, hw, c, groups)
+        assert status == 5 or status == 1  # no workspace where some is needed, or no y
