@@ -474,6 +474,13 @@ def _type(dtype: torch.dtype) -> int:
     return t
 
 
+def _fits(*values: int) -> None:
+    """The library takes these as int32, and ctypes would pass a larger one modulo 2^32."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{v} does not fit 32 bits")
+
+
 def _on_device(*ts) -> int:
     """The device of the tensors given: one GPU, the current one (the library launches there)."""
     index = ts[0].get_device()
@@ -582,6 +589,7 @@ def mx4_quantize(x: torch.Tensor, out: Optional[Mx4] = None, stream=None) -> Mx4
     """x [..., k] (float32, bfloat16 or float16) rounded to microscaled 4-bit codes, a row per leading
     index (ifx_mx4_quantize)."""
     rows, k, ld = _pitch(x)
+    _fits(rows, k)
     if out is None:
         index = _on_device(x)
         out = _mx4_like(rows, k, x, stream)
@@ -599,6 +607,7 @@ def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16, out: Optional[to
     """The values of a microscaled tensor, [rows, k] (ifx_mx4_dequantize)."""
     index = _on_device(q.codes, q.scales, out)
     rows, k = _mx4_check(q, "q"), q.k
+    _fits(rows, k)
     ld = k
     if out is None:
         out = _alloc(q.codes, stream, dtype, rows, k)
@@ -620,6 +629,7 @@ def mx4_matmul(a: Mx4, w: Mx4, bias: Optional[torch.Tensor] = None, residual: Op
     m, n = _mx4_check(a, "a"), _mx4_check(w, "w")
     if a.k != w.k:
         raise ValueError(f"a of {a.k} columns, w of {w.k}")
+    _fits(m, n, a.k, act)
     _param(bias, n, "bias")
     ld_y = ld_res = n
     if out is None:
@@ -646,6 +656,7 @@ def _gn_desc(x: torch.Tensor, groups: int, act: int, eps: float) -> GnDesc:
     hw = 1
     for size in x.shape[1:-1]:
         hw *= size
+    _fits(x.shape[0], hw, x.shape[-1], groups, act)
     return GnDesc(x.shape[0], hw, x.shape[-1], groups, _type(x.dtype), act, eps, ld, ld, ld)
 
 

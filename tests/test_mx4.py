@@ -460,3 +460,35 @@ def test_offsets_past_32_bits():
     few = (t.codes.cpu().numpy(), t.scales.cpu().numpy())
     check_product(y[-40:], 40, 24, k, few, (w.codes.cpu().numpy(), w.scales.cpu().numpy()), None, None, 0, "bf16")
     assert not y[:-40].any()
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """The C entry points take 32-bit sizes: a larger tensor is refused by the binding, not taken modulo 2^32.  The
+    tensors are on no device and have no memory, so a call that went on would be refused for its NULL pointers."""
+    monkeypatch.setattr(ifx, "_on_device", lambda *ts: 0)
+    monkeypatch.setattr(ifx, "_raw_stream", lambda stream, index: 0)
+
+    def meta(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    def mx4(rows, k):
+        k1 = (k + 127) // 128
+        return ifx.Mx4(meta(k1, rows, 64, dtype=torch.uint8), meta(k1, rows, 4, dtype=torch.uint8), k)
+    big, fit = (1 << 32) + 5, 5
+    calls = [lambda b: ifx.mx4_quantize(meta(b, 3)), lambda b: ifx.mx4_quantize(meta(3, b)),
+             lambda b: ifx.mx4_quantize(meta(b, 3), out=mx4(b, 3)),
+             lambda b: ifx.mx4_dequantize(mx4(b, 3)), lambda b: ifx.mx4_dequantize(mx4(3, b)),
+             lambda b: ifx.mx4_matmul(mx4(b, 3), mx4(4, 3)), lambda b: ifx.mx4_matmul(mx4(4, 3), mx4(b, 3)),
+             lambda b: ifx.mx4_matmul(mx4(4, b), mx4(4, b)), lambda b: ifx.mx4_matmul(mx4(4, 3), mx4(4, 3), act=b - fit),
+             lambda b: ifx.group_norm(meta(b, 2, 8), 4), lambda b: ifx.group_norm(meta(2, b, 8), 4),
+             lambda b: ifx.group_norm(meta(2, 3, b - 1), 4), lambda b: ifx.group_norm(meta(2, 3, 8), b - 1),
+             lambda b: ifx.group_norm(meta(2, 3, 8), 4, act=b - fit),
+             lambda b: ifx.group_norm_mx4(meta(b, 2, 8), 4), lambda b: ifx.group_norm_mx4(meta(2, b, 8), 4),
+             lambda b: ifx.group_norm_backward(meta(b, 2, 8), meta(b, 2, 8), meta(b, 4), meta(b, 4), 4),
+             lambda b: ifx.group_norm_backward(meta(2, b, 8), meta(2, b, 8), meta(2, 4), meta(2, 4), 4)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ifx.IfxError, match="NULL"):
+            call(fit)
+        with pytest.raises(ValueError, match="32 bits"):
+            call(big)
+            pytest.fail(f"call {i}")
