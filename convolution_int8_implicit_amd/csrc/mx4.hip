@@ -56,10 +56,10 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *x, long l
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = raw[i].get(e);
-        if (col + 8 > k) {
+        if (k - col < 8) {  // (col + 8 may pass 32 bits)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (col + e >= k) f[e] = 0.0f;
+                if (e >= k - col) f[e] = 0.0f;
         }
         unsigned s;
         const unsigned r = mx4_codes(f, s);
@@ -205,7 +205,7 @@ void launch_rows(const Mx4Args &a, hipStream_t s)
 hipError_t launch_mx4_quantize(const void *x, int type, long long ld, int rows, int k, uint8_t *codes, uint8_t *scales,
                                hipStream_t s)
 {
-    const int k1 = (k + 127) / 128, groups = (k1 + kQPanels - 1) / kQPanels;
+    const int k1 = (k - 1) / 128 + 1, groups = (k1 - 1) / kQPanels + 1;
     const dim3 grid((unsigned)((rows + kQRows - 1LL) / kQRows * groups));
     const bool once = ld % 64 == 0 && ((uintptr_t)x & 127) == 0;
     auto *f = type == 0   ? mx4_quantize_kernel<0, false>
@@ -218,7 +218,7 @@ hipError_t launch_mx4_quantize(const void *x, int type, long long ld, int rows, 
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int k, void *y, int type,
                                  long long ld, hipStream_t s)
 {
-    const int k1 = (k + 127) / 128, groups = (k1 + kQPanels - 1) / kQPanels;
+    const int k1 = (k - 1) / 128 + 1, groups = (k1 - 1) / kQPanels + 1;
     const dim3 grid((unsigned)((rows + kQRows - 1LL) / kQRows * groups));
     auto *f = type == 0 ? mx4_dequantize_kernel<0> : type == 1 ? mx4_dequantize_kernel<1> : mx4_dequantize_kernel<2>;
     const int past = stored_past(y, rows, ld, type == 0 ? 4 : 2);

@@ -492,3 +492,31 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
         with pytest.raises(ValueError, match="32 bits"):
             call(big)
             pytest.fail(f"call {i}")
+
+
+@pytest.mark.gpu
+def test_longest_rows():
+    """One row of 2^31 - 1 columns, the most that an int32 counts: the last panels, whose end and padding lie past
+    where a column number plus a few passes 31 bits, and nothing in the panels before them."""
+    k = (1 << 31) - 1
+    k1 = (k - 1) // 128 + 1
+    first = (k1 - 4) * 128
+    note(f"one row of {k} columns")
+    x = torch.zeros(1, k, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x[:, first:] = torch.randn(1, k - first, device="cuda", generator=gen)
+    codes, scales = lowp.mx4_quantize(f64(x[:, first:]))
+    note("rounding")
+    q = ifx.mx4_quantize(x)
+    assert q.codes.shape == (k1, 1, 64)
+    assert np.array_equal(q.codes[-4:].cpu().numpy(), codes) and np.array_equal(q.scales[-4:].cpu().numpy(), scales)
+    assert not q.codes[:-4].any() and not q.scales[:-4].any()
+    del x
+    note("values")
+    v = ifx.mx4_dequantize(q)
+    assert np.array_equal(f64(v[:, first:]), lowp.mx4_values(codes, scales, k - first)) and not v[:, :first].any()
+    del v
+    note("product")
+    exact, _, s = lowp.mx4_matmul((codes, scales), (codes, scales), k - first)
+    # the other panels add zeros: no rounding of theirs
+    assert excess(f64(ifx.mx4_matmul(q, q, dtype=torch.float32)), exact, (4 + 18) * 2.0 ** -23 * s, "f32") == 0
