@@ -158,7 +158,8 @@ class NormPointwise4:
     def features(self, acc: torch.Tensor, stream=None) -> torch.Tensor:
         """float32 features of int32 accumulators [n, h, w, c], memory of the stream that computes them."""
         out = _alloc(acc, stream, torch.float32, *acc.shape)
-        return dequantize_i32(acc, self.scale, out=out, stream=stream)
+        # (an empty tensor has no address, which the call refuses)
+        return dequantize_i32(acc, self.scale, out=out, stream=stream) if acc.numel() else out
 
     def forward(self, acc: torch.Tensor, residual: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
                 stream=None) -> torch.Tensor:
@@ -166,9 +167,9 @@ class NormPointwise4:
         q = group_norm_mx4(self.features(acc, stream), self.groups, self.norm_weight, self.norm_bias, self.eps, self.act,
                            stream=stream)
         if residual is not None:
-            residual = residual.view(q.rows, -1)
+            residual = residual.view(q.rows, self.weight.rows)
         y = mx4_matmul(q, self.weight, self.bias, residual, self.out_act, dtype, stream=stream)
-        return y.view(*acc.shape[:-1], -1)
+        return y.view(*acc.shape[:-1], self.weight.rows)
 
     def norm(self, x: torch.Tensor, stream=None):
         """(y, mean, rstd) of the normalisation alone."""

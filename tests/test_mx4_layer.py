@@ -130,3 +130,19 @@ def test_layer_on_a_given_stream():
         torch.cuda.synchronize()
         assert torch.equal(y, expect)
         del fill
+
+
+@pytest.mark.gpu
+def test_layer_of_no_images():
+    """A batch of none gives a result of none, with and without a residual and on a given stream."""
+    layer, acc, *_ = layer_and_input(1)
+    none = acc[:0]
+    shape = (0, *acc.shape[1:3], 96)
+    y = layer.forward(none)
+    assert y.shape == shape and y.dtype == torch.bfloat16
+    res = torch.empty(shape, dtype=torch.float32, device="cuda")
+    assert layer.forward(none, res, torch.float32, stream=torch.cuda.Stream()).shape == shape
+    x = layer.features(none)
+    assert x.shape == none.shape and x.dtype == torch.float32
+    out, mean, rstd = layer.norm(x)
+    assert out.shape == x.shape and mean.shape == (0, 32)
