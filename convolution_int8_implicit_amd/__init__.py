@@ -12,7 +12,7 @@ Entry points mirror include/ifx.h:
     block_workspace_bytes, block_forward, net_workspace_bytes, net_forward,
     fold_bn, status_string, last_hip_error, version,
     mx4_quantize, mx4_dequantize, mx4_matmul (microscaled 4-bit floating point),
-    group_norm, group_norm_mx4, group_norm_backward (channels last)
+    group_norm, group_norm_mx4, group_norm_backward, group_norm_kernel_name (channels last)
 """
 from __future__ import annotations
 
@@ -684,7 +684,8 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
                bias: Optional[torch.Tensor] = None, eps: float = 1e-5, act: int = ACT_NONE,
                out: Optional[torch.Tensor] = None, stream=None):
     """Group norm of channels-last x [n, ..., c] with an activation (ifx_group_norm) ->
-    (y, mean [n, groups], rstd [n, groups])."""
+    (y, mean [n, groups], rstd [n, groups]).  As every call here it records nothing for autograd: the results
+    require no gradient, group_norm_backward gives it."""
     index = _on_device(x, weight, bias, out)
     d = _gn_desc(x, groups, act, eps)
     _param(weight, d.c, "weight")

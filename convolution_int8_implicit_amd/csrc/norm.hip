@@ -8,10 +8,10 @@
 // What bounds it: memory (each value read and written once in the slab form), closely followed by the
 // vector units: about 19 operations a value with SiLU, whose exponential and reciprocal cost four
 // each.  Hence the activation chosen outside the loops, z as one subtraction and one fused multiply-add, and addresses by
-// uniform strides.  bf16 with SiLU: 128 x 784 x 512
-// 41 us, 4.9-5.2 TB/s of the 5.2 that a copy reaches; 128 x 3136 x 256, one slab of 1024 threads a CU so that loads,
-// sums and stores take turns, 107-110 us, 3.7 TB/s; the 4-bit form of the former 39 us, vector-bound.  Split form:
-// 1 x 16384 x 512 20 us.
+// uniform strides.  With SiLU, on one tensor / on three in turn (the memory-side cache holds part of the one):
+// 128 x 784 x 512 bf16 43 / 51 us, 4.8 / 4.1 TB/s of the 5.2 that a copy reaches, float32 87 / 87, 4.7; 128 x 3136 x 256 bf16,
+// one slab of 1024 threads a CU so that loads, sums and stores take turns, 108 / 109 us, 3.8 TB/s; the 4-bit form of the first
+// 41 / 45 us, its vector units active 91 % of the time, in float32 43 / 57.  Split form: 1 x 16384 x 512 bf16 20 / 22 us.
 #include <algorithm>
 #include <iterator>
 

@@ -145,7 +145,8 @@ class NormPointwise4:
 
     weight float [c_out, c] is rounded once; norm_weight, norm_bias float32 [c]; bias float32 [c_out] or
     None.  forward() serves; norm() and norm_backward() are the layer's normalisation alone with its gradient,
-    for fitting norm_weight and norm_bias to the quantised features.
+    for fitting norm_weight and norm_bias to the quantised features.  A result of a call with a stream is memory of
+    that stream.
     """
 
     def __init__(self, weight: torch.Tensor, norm_weight: torch.Tensor, norm_bias: torch.Tensor, groups: int,
