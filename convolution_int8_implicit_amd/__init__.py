@@ -12,7 +12,10 @@ Entry points mirror include/ifx.h:
     block_workspace_bytes, block_forward, net_workspace_bytes, net_forward,
     fold_bn, status_string, last_hip_error, version,
     mx4_quantize, mx4_dequantize, mx4_matmul (microscaled 4-bit floating point),
-    group_norm, group_norm_mx4, group_norm_backward, group_norm_kernel_name (channels last)
+    group_norm, group_norm_mx4, group_norm_backward, group_norm_kernel_name (channels last),
+    fp8_quantize, fp8_quantize_t, fp8_dequantize, fp8_matmul (8-bit floating point, a power of two per block of 128),
+    gated, gated_fp8, gated_backward (both projections of a gated feed-forward layer),
+    rms_norm, rms_norm_fp8, rms_norm_backward
 """
 from __future__ import annotations
 
@@ -32,6 +35,8 @@ __all__ = [
     "net_forward", "NetGraph", "fold_bn", "BnFold", "status_string", "last_hip_error", "version", "LIB_PATH",
     "ACT_NONE", "ACT_RELU", "ACT_SILU", "Mx4", "mx4_empty", "mx4_quantize", "mx4_dequantize", "mx4_matmul",
     "group_norm", "group_norm_mx4", "group_norm_backward", "GnDesc", "group_norm_kernel_name",
+    "FP8_E4M3", "FP8_E5M2", "Fp8", "fp8_empty", "fp8_quantize", "fp8_quantize_t", "fp8_dequantize", "fp8_matmul",
+    "gated", "gated_fp8", "gated_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward",
 ]
 
 RELU, RESIDUAL, MAXPOOL, OUT_I32, INPUT_NHWC, OUT_EVEN, OUT_PHASE, IN_PHASE = 1, 2, 4, 8, 16, 32, 64, 128
@@ -89,6 +94,22 @@ class GnDesc(ctypes.Structure):
                 ("ld_y", ctypes.c_int64), ("ld_dy", ctypes.c_int64)]
 
 
+class Fp8Desc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("a_format", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("act", ctypes.c_int32), ("ld_y", ctypes.c_int64), ("ld_res", ctypes.c_int64)]
+
+
+class GatedDesc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("ld_y", ctypes.c_int64), ("ld_up", ctypes.c_int64), ("ld_dy", ctypes.c_int64)]
+
+
+class RmsDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("c", ctypes.c_int32), ("type", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("ld_x", ctypes.c_int64), ("ld_res", ctypes.c_int64), ("ld_h", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_dy", ctypes.c_int64), ("ld_dh", ctypes.c_int64)]
+
+
 _LIB = None
 
 
@@ -144,6 +165,20 @@ def lib() -> ctypes.CDLL:
         "ifx_group_norm_mx4": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
         "ifx_group_norm_backward": ([ctypes.POINTER(GnDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
         "ifx_group_norm_kernel_name": ([ctypes.POINTER(GnDesc), i32, ctypes.c_char_p, sz], i32),
+        "ifx_fp8_code_bytes": ([i32, i32], sz),
+        "ifx_fp8_scale_bytes": ([i32, i32], sz),
+        "ifx_fp8_quantize": ([vp, i32, i64, i32, i32, i32, vp, vp, vp], i32),
+        "ifx_fp8_quantize_t": ([vp, i32, i64, i32, i32, i32, vp, vp, vp], i32),
+        "ifx_fp8_dequantize": ([vp, vp, i32, i32, i32, vp, i32, i64, vp], i32),
+        "ifx_fp8_matmul": ([ctypes.POINTER(Fp8Desc), vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        "ifx_gated_workspace_bytes": ([ctypes.POINTER(GatedDesc)], sz),
+        "ifx_gated": ([ctypes.POINTER(GatedDesc), vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        "ifx_gated_fp8": ([ctypes.POINTER(GatedDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "ifx_gated_backward": ([ctypes.POINTER(GatedDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        "ifx_rms_norm_workspace_bytes": ([ctypes.POINTER(RmsDesc)], sz),
+        "ifx_rms_norm": ([ctypes.POINTER(RmsDesc), vp, vp, vp, vp, vp, vp, vp], i32),
+        "ifx_rms_norm_fp8": ([ctypes.POINTER(RmsDesc), vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        "ifx_rms_norm_backward": ([ctypes.POINTER(RmsDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
         "ifx_status_string": ([i32], ctypes.c_char_p),
         "ifx_probe_copy": ([vp, vp, sz, vp], i32),
         "ifx_probe_mfma_i8": ([vp, i32, i32, vp], i32),
@@ -748,6 +783,276 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                                          _addr(bias), out.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), _addr(ws),
                                          nbytes, _raw_stream(stream, index)), "ifx_group_norm_backward")
     return out, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point tensors, the gated projections and root mean square norm
+# ---------------------------------------------------------------------------
+#: The 8-bit formats: four exponent and three mantissa bits (up to 448), five and two (up to 57344).
+FP8_E4M3, FP8_E5M2 = 0, 1
+
+
+class Fp8(NamedTuple):
+    """An 8-bit floating point tensor of codes.shape[1] rows and k columns (layout: include/ifx.h):
+    codes uint8 [ceil(k / 128), rows, 128], scales uint8 [ceil(k / 512), rows, 4]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    k: int
+    format: int = FP8_E4M3
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[1]
+
+
+def _fp8_like(rows: int, k: int, format: int, like: torch.Tensor, stream) -> Fp8:
+    return Fp8(_alloc(like, stream, torch.uint8, (k + 127) // 128, rows, 128),
+               _alloc(like, stream, torch.uint8, (k + 511) // 512, rows, 4), k, format)
+
+
+def fp8_empty(rows: int, k: int, format: int = FP8_E4M3, device="cuda") -> Fp8:
+    """Uninitialised codes and scales, for the `out` of a call."""
+    return Fp8(torch.empty(((k + 127) // 128, rows, 128), dtype=torch.uint8, device=device),
+               torch.empty(((k + 511) // 512, rows, 4), dtype=torch.uint8, device=device), k, format)
+
+
+def _fp8_check(q: Fp8, name: str) -> int:
+    """The rows of q."""
+    codes, scales, k, _ = q
+    k1, k4 = (k + 127) // 128, (k + 511) // 512
+    rows = codes.shape[1] if codes.dim() == 3 else -1
+    if (codes.shape != (k1, rows, 128) or scales.shape != (k4, rows, 4) or codes.dtype != torch.uint8
+            or scales.dtype != torch.uint8 or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError(f"{name}: contiguous uint8 codes [{k1}, rows, 128] and scales [{k4}, rows, 4] expected for k = {k}")
+    return rows
+
+
+def _fp8_out(out: Optional[Fp8], rows: int, k: int, format: int, like: torch.Tensor, stream) -> Fp8:
+    """`out`, which has to be of these sizes and this format, or a new tensor."""
+    if out is None:
+        return _fp8_like(rows, k, format, like, stream)
+    if _fp8_check(out, "out") != rows or out.k != k or out.format != format:
+        raise ValueError(f"out of {out.rows} x {out.k} in format {out.format}, {rows} x {k} in format {format} expected")
+    return out
+
+
+def _e4m3(q: Fp8, name: str) -> None:
+    if q.format != FP8_E4M3:
+        raise ValueError(f"{name}: format FP8_E4M3 expected")
+
+
+def _out_parts(out: Optional[Fp8]):
+    return out[:2] if out is not None else ()
+
+
+def fp8_quantize(x: torch.Tensor, format: int = FP8_E4M3, out: Optional[Fp8] = None, stream=None) -> Fp8:
+    """x [..., k] (float32, bfloat16 or float16) rounded to 8 bits with a power of two per block of 128 columns, a row
+    per leading index (ifx_fp8_quantize)."""
+    rows, k, ld = _pitch(x)
+    _fits(rows, k, format)
+    index = _on_device(x, *_out_parts(out))
+    out = _fp8_out(out, rows, k, format, x, stream)
+    _check(lib().ifx_fp8_quantize(x.data_ptr(), _type(x.dtype), ld, rows, k, format, out.codes.data_ptr(),
+                                  out.scales.data_ptr(), _raw_stream(stream, index)), "ifx_fp8_quantize")
+    return out
+
+
+def fp8_quantize_t(x: torch.Tensor, format: int = FP8_E4M3, out: Optional[Fp8] = None, stream=None) -> Fp8:
+    """The transpose of x [..., n], a row per column of x, blocks of 128 consecutive leading indices
+    (ifx_fp8_quantize_t)."""
+    k, rows, ld = _pitch(x)
+    if rows == 0:  # an empty tensor has no rows to _pitch
+        k = 1
+        for size in x.shape[:-1]:
+            k *= size
+    _fits(rows, k, format)
+    index = _on_device(x, *_out_parts(out))
+    out = _fp8_out(out, rows, k, format, x, stream)
+    _check(lib().ifx_fp8_quantize_t(x.data_ptr(), _type(x.dtype), ld, rows, k, format, out.codes.data_ptr(),
+                                    out.scales.data_ptr(), _raw_stream(stream, index)), "ifx_fp8_quantize_t")
+    return out
+
+
+def fp8_dequantize(q: Fp8, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The values of an 8-bit tensor, [rows, k] (ifx_fp8_dequantize)."""
+    index = _on_device(q.codes, q.scales, out)
+    rows, k = _fp8_check(q, "q"), q.k
+    _fits(rows, k, q.format)
+    ld = k
+    if out is None:
+        out = _alloc(q.codes, stream, dtype, rows, k)
+    else:
+        if out.shape != (rows, k):
+            raise ValueError(f"out of shape {tuple(out.shape)}, q of {rows} x {k}")
+        ld = _pitch(out)[2]
+    _check(lib().ifx_fp8_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.format, rows, k, out.data_ptr(),
+                                    _type(out.dtype), ld, _raw_stream(stream, index)), "ifx_fp8_dequantize")
+    return out
+
+
+def fp8_matmul(a: Fp8, w: Fp8, bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+               act: int = ACT_NONE, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """act(a @ w.T + bias + residual), [a.rows, w.rows] (ifx_fp8_matmul); a in either format, w in FP8_E4M3; bias
+    float32 [w.rows], residual of the output's type and shape."""
+    index = _on_device(a.codes, a.scales, w.codes, w.scales, bias, residual, out)
+    m, n = _fp8_check(a, "a"), _fp8_check(w, "w")
+    if a.k != w.k:
+        raise ValueError(f"a of {a.k} columns, w of {w.k}")
+    _e4m3(w, "w")
+    _fits(m, n, a.k, act, a.format)
+    _param(bias, n, "bias")
+    ld_y = ld_res = n
+    if out is None:
+        out = _alloc(a.codes, stream, dtype, m, n)
+    else:
+        if out.shape != (m, n):
+            raise ValueError(f"out of shape ({m}, {n}) expected")
+        ld_y = _pitch(out)[2]
+    if residual is not None:
+        if residual.shape != (m, n) or residual.dtype != out.dtype:
+            raise ValueError(f"residual of shape ({m}, {n}) and {out.dtype} expected")
+        ld_res = _pitch(residual)[2]
+    d = Fp8Desc(m, n, a.k, a.format, _type(out.dtype), act, ld_y, ld_res)
+    _check(lib().ifx_fp8_matmul(d, a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+                                _addr(bias), _addr(residual), out.data_ptr(), _raw_stream(stream, index)),
+           "ifx_fp8_matmul")
+    return out
+
+
+def _gated_desc(x: Fp8, w_gate: Fp8, w_up: Fp8, act: int, dtype: torch.dtype) -> GatedDesc:
+    m, n = _fp8_check(x, "x"), _fp8_check(w_gate, "w_gate")
+    if _fp8_check(w_up, "w_up") != n or not x.k == w_gate.k == w_up.k:
+        raise ValueError(f"x of {x.k} columns, w_gate of {n} x {w_gate.k}, w_up of {w_up.rows} x {w_up.k}")
+    for q, name in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
+        _e4m3(q, name)
+    _fits(m, n, x.k, act)
+    return GatedDesc(m, n, x.k, _type(dtype), act, n, n, n)
+
+
+def _gated_addrs(x: Fp8, w_gate: Fp8, w_up: Fp8):
+    return (x.codes.data_ptr(), x.scales.data_ptr(), w_gate.codes.data_ptr(), w_gate.scales.data_ptr(),
+            w_up.codes.data_ptr(), w_up.scales.data_ptr())
+
+
+def gated(x: Fp8, w_gate: Fp8, w_up: Fp8, act: int = ACT_SILU, dtype: torch.dtype = torch.bfloat16,
+          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """act(x @ w_gate.T) * (x @ w_up.T), [x.rows, w_gate.rows], in one kernel (ifx_gated); all in FP8_E4M3."""
+    index = _on_device(*x[:2], *w_gate[:2], *w_up[:2], out)
+    d = _gated_desc(x, w_gate, w_up, act, dtype if out is None else out.dtype)
+    if out is None:
+        out = _alloc(x.codes, stream, dtype, d.m, d.n)
+    else:
+        if out.shape != (d.m, d.n):
+            raise ValueError(f"out of shape ({d.m}, {d.n}) expected")
+        d.ld_y = _pitch(out)[2]
+    _check(lib().ifx_gated(d, *_gated_addrs(x, w_gate, w_up), out.data_ptr(), _raw_stream(stream, index)), "ifx_gated")
+    return out
+
+
+def gated_fp8(x: Fp8, w_gate: Fp8, w_up: Fp8, act: int = ACT_SILU, out: Optional[Fp8] = None, stream=None) -> Fp8:
+    """gated whose result is rounded to 8 bits (FP8_E4M3) instead of being stored (ifx_gated_fp8): the operand of the
+    projection back."""
+    index = _on_device(*x[:2], *w_gate[:2], *w_up[:2], *_out_parts(out))
+    d = _gated_desc(x, w_gate, w_up, act, torch.float32)
+    out = _fp8_out(out, d.m, d.n, FP8_E4M3, x.codes, stream)
+    nbytes = lib().ifx_gated_workspace_bytes(d)
+    ws = _alloc(x.codes, stream, torch.uint8, nbytes) if nbytes else None
+    _check(lib().ifx_gated_fp8(d, *_gated_addrs(x, w_gate, w_up), out.codes.data_ptr(), out.scales.data_ptr(), _addr(ws),
+                               nbytes, _raw_stream(stream, index)), "ifx_gated_fp8")
+    return out
+
+
+def gated_backward(dy: torch.Tensor, x: Fp8, w_gate: Fp8, w_up: Fp8, act: int = ACT_SILU, out=None, stream=None):
+    """Gradient of gated at its two projections, which are computed anew (ifx_gated_backward) ->
+    (dgate, dup) of dy's type and shape; out: a pair of such tensors.  The gradients of x and of the weights are
+    products of these (fp8_quantize, fp8_quantize_t, fp8_matmul)."""
+    index = _on_device(dy, *x[:2], *w_gate[:2], *w_up[:2], *(out if out is not None else ()))
+    d = _gated_desc(x, w_gate, w_up, act, dy.dtype)
+    if dy.shape != (d.m, d.n):
+        raise ValueError(f"dy of shape ({d.m}, {d.n}) expected")
+    d.ld_dy = _pitch(dy)[2]
+    if out is None:
+        out = (_alloc(dy, stream, dy.dtype, d.m, d.n), _alloc(dy, stream, dy.dtype, d.m, d.n))
+    else:
+        d.ld_y, d.ld_up = _like(out[0], dy, "out[0]"), _like(out[1], dy, "out[1]")
+    _check(lib().ifx_gated_backward(d, dy.data_ptr(), *_gated_addrs(x, w_gate, w_up), out[0].data_ptr(), out[1].data_ptr(),
+                                    _raw_stream(stream, index)), "ifx_gated_backward")
+    return out
+
+
+def _rms_desc(x: torch.Tensor, eps: float) -> RmsDesc:
+    rows, c, ld = _pitch(x)
+    _fits(rows, c)
+    return RmsDesc(rows, c, _type(x.dtype), eps, ld, c, c, c, c, c)
+
+
+def _rms_forward(x, weight, residual, eps, sum_out, stream):
+    """The descriptor, the sum (x itself without a residual, unless sum_out is given) and whether it is written."""
+    d = _rms_desc(x, eps)
+    _param(weight, d.c, "weight")
+    if residual is not None:
+        d.ld_res = _like(residual, x, "residual")
+    if sum_out is not None:
+        d.ld_h = _like(sum_out, x, "sum_out")
+        return d, sum_out, True
+    return (d, x, False) if residual is None else (d, _alloc(x, stream, x.dtype, *x.shape), True)
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-5, out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None, stream=None):
+    """Root mean square norm of h = x + residual over the last axis (ifx_rms_norm) -> (y, h, rstd): y and h of x's
+    shape and type, rstd float32 [rows].  Without a residual h is x itself.  sum_out may be x or the residual, out may
+    be either too, but not sum_out.  Records nothing for autograd: rms_norm_backward gives the gradient."""
+    index = _on_device(x, weight, residual, out, sum_out)
+    d, h, written = _rms_forward(x, weight, residual, eps, sum_out, stream)
+    if out is None:
+        out = _alloc(x, stream, x.dtype, *x.shape)
+    else:
+        d.ld_y = _like(out, x, "out")
+    rstd = _alloc(x, stream, torch.float32, d.rows)
+    _check(lib().ifx_rms_norm(d, x.data_ptr(), _addr(residual), _addr(weight), h.data_ptr() if written else None,
+                              out.data_ptr(), rstd.data_ptr(), _raw_stream(stream, index)), "ifx_rms_norm")
+    return out, h, rstd
+
+
+def rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 eps: float = 1e-5, out: Optional[Fp8] = None, sum_out: Optional[torch.Tensor] = None, stream=None):
+    """rms_norm whose result is rounded to 8 bits (FP8_E4M3) instead of being stored, a row per leading index
+    (ifx_rms_norm_fp8) -> (q, h, rstd)."""
+    index = _on_device(x, weight, residual, sum_out, *_out_parts(out))
+    d, h, written = _rms_forward(x, weight, residual, eps, sum_out, stream)
+    out = _fp8_out(out, d.rows, d.c, FP8_E4M3, x, stream)
+    rstd = _alloc(x, stream, torch.float32, d.rows)
+    _check(lib().ifx_rms_norm_fp8(d, x.data_ptr(), _addr(residual), _addr(weight), h.data_ptr() if written else None,
+                                  out.codes.data_ptr(), out.scales.data_ptr(), rstd.data_ptr(),
+                                  _raw_stream(stream, index)), "ifx_rms_norm_fp8")
+    return out, h, rstd
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      dh: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of rms_norm (ifx_rms_norm_backward) -> (dx, dweight [c]) from the forward pass's h and rstd; dh is
+    what reaches h past the norm.  dx is x's and the residual's; dweight is float32, also where weight is None (1)."""
+    index = _on_device(dy, h, rstd, weight, dh, out)
+    d = _rms_desc(h, 0.0)
+    _param(weight, d.c, "weight")
+    _param(rstd, d.rows, "rstd")
+    d.ld_dy = _like(dy, h, "dy")
+    if dh is not None:
+        d.ld_dh = _like(dh, h, "dh")
+    if out is None:
+        out = _alloc(h, stream, h.dtype, *h.shape)
+    else:
+        d.ld_y = _like(out, h, "out")
+    dweight = _alloc(h, stream, torch.float32, d.c)
+    nbytes = lib().ifx_rms_norm_workspace_bytes(d)
+    ws = _alloc(h, stream, torch.uint8, nbytes) if nbytes else None
+    _check(lib().ifx_rms_norm_backward(d, dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), _addr(weight), _addr(dh),
+                                       out.data_ptr(), dweight.data_ptr(), _addr(ws), nbytes, _raw_stream(stream, index)),
+           "ifx_rms_norm_backward")
+    return out, dweight
 
 
 class NetGraph:

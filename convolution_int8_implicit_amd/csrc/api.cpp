@@ -1476,3 +1476,326 @@ ifx_status ifx_group_norm_kernel_name(const ifx_gn_desc *d, int32_t form, char *
 }
 
 }  // extern "C"
+
+// ----------------------------------------------------------------------------
+// 8-bit floating point tensors, the gated projections and root mean square norm
+// ----------------------------------------------------------------------------
+namespace {
+
+inline bool known_format(int32_t f) { return f == IFX_FP8_E4M3 || f == IFX_FP8_E5M2; }
+
+// Rows, columns and grid of an 8-bit tensor (of 16 rows of four panels a workgroup, as the 4-bit ones).
+ifx_status check_fp8(int32_t rows, int32_t k) { return check_mx4(rows, k); }
+
+ifx_status check_fp8_rows(const void *x, int32_t type, int64_t ld, int64_t x_rows, int64_t x_cols, int32_t rows, int32_t k,
+                          int32_t format, const uint8_t *codes, const uint8_t *scales)
+{
+    if (!known_type(type) || !known_format(format)) return IFX_E_UNSUPPORTED;
+    ifx_status st = check_fp8(rows, k);
+    if (st != IFX_OK) return st;
+    if (!pitch_ok(x_rows, x_cols, ld)) return IFX_E_SHAPE;
+    if (rows == 0) return IFX_OK;
+    if (!x) return IFX_E_NULL;
+    st = check_codes(codes, scales);
+    if (st != IFX_OK) return st;
+    return aligned_to(x, type_bytes(type)) ? IFX_OK : IFX_E_ALIGN;
+}
+
+// Sizes of a product of m rows and n columns in tiles of at least 64 x 64.
+ifx_status check_product(int32_t m, int32_t n, int32_t k)
+{
+    if (m < 0 || n < 0) return IFX_E_SHAPE;
+    ifx_status st = check_fp8(m, k);
+    if (st == IFX_OK) st = check_fp8(n, k);
+    if (st != IFX_OK) return st;
+    return (m + 63LL) / 64 * ((n + 63LL) / 64) > 0xffffffffLL / 256 - 8 ? IFX_E_SHAPE : IFX_OK;
+}
+
+// What the three gated calls share: sizes and operands.
+ifx_status check_gated(const ifx_gated_desc *d, const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *g_codes,
+                       const uint8_t *g_scales, const uint8_t *u_codes, const uint8_t *u_scales)
+{
+    if (!d) return IFX_E_NULL;
+    if (!known_type(d->type) || !known_act(d->act)) return IFX_E_UNSUPPORTED;
+    ifx_status st = check_product(d->m, d->n, d->k);
+    if (st != IFX_OK || d->m == 0 || d->n == 0) return st;
+    st = check_codes(x_codes, x_scales);
+    if (st == IFX_OK) st = check_codes(g_codes, g_scales);
+    if (st == IFX_OK) st = check_codes(u_codes, u_scales);
+    return st;
+}
+
+ifx::Fp8Args gated_args(const ifx_gated_desc *d, const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *g_codes,
+                        const uint8_t *g_scales, const uint8_t *u_codes, const uint8_t *u_scales)
+{
+    ifx::Fp8Args a = {};
+    a.a_codes = x_codes;
+    a.a_scales = x_scales;
+    a.w_codes = g_codes;
+    a.w_scales = g_scales;
+    a.u_codes = u_codes;
+    a.u_scales = u_scales;
+    a.m = d->m;
+    a.n = d->n;
+    a.k1 = (d->k - 1) / 128 + 1;
+    a.type = d->type;
+    a.act = d->act;
+    a.ld_y = d->ld_y;
+    return a;
+}
+
+size_t gated_workspace(int32_t m, int32_t n) { return ifx::fp8_few_rows(m, n) ? (size_t)m * n * 4 : 0; }
+
+ifx_status check_rms(const ifx_rms_desc *d)
+{
+    if (!d) return IFX_E_NULL;
+    if (!known_type(d->type)) return IFX_E_UNSUPPORTED;
+    if (d->rows < 0 || d->c < 1 || !(d->eps >= 0.0f)) return IFX_E_SHAPE;
+    if (d->c > 24576) return IFX_E_UNSUPPORTED;
+    // work-items of a launch
+    const int64_t threads = d->c <= 128 ? 16 : d->c <= 1024 ? 64 : d->c <= 8192 ? 256 : 1024;
+    if (d->rows > 1024 && d->rows * threads > 0xffffffffLL - 1024) return IFX_E_SHAPE;
+    return pitch_ok(d->rows, d->c, d->ld_x) ? IFX_OK : IFX_E_SHAPE;
+}
+
+// A further operand of d's rows that is there: its pitch, then its alignment.
+ifx_status check_operand(const ifx_rms_desc *d, const void *p, int64_t ld)
+{
+    if (!p) return IFX_OK;
+    if (!pitch_ok(d->rows, d->c, ld)) return IFX_E_SHAPE;
+    return aligned_to(p, type_bytes(d->type)) ? IFX_OK : IFX_E_ALIGN;
+}
+
+// What the two forward norms share; the arguments but the results'.
+ifx_status check_rms_forward(const ifx_rms_desc *d, const void *x, const void *residual, const float *weight, const void *h,
+                             const float *rstd, ifx::RmsArgs *a)
+{
+    ifx_status st = check_rms(d);
+    if (st != IFX_OK || d->rows == 0) return st;
+    if (!x) return IFX_E_NULL;
+    st = check_operand(d, x, d->ld_x);
+    if (st == IFX_OK) st = check_operand(d, residual, d->ld_res);
+    if (st == IFX_OK) st = check_operand(d, h, d->ld_h);
+    if (st != IFX_OK) return st;
+    if (!aligned_to(weight, 4) || !aligned_to(rstd, 4)) return IFX_E_ALIGN;
+    *a = {};
+    a->x = x;
+    a->res = residual;
+    a->h = const_cast<void *>(h);
+    a->weight = weight;
+    a->rstd = const_cast<float *>(rstd);
+    a->rows = d->rows;
+    a->c = d->c;
+    a->type = d->type;
+    a->eps = d->eps;
+    a->ld_x = d->ld_x;
+    a->ld_res = d->ld_res;
+    a->ld_h = d->ld_h;
+    a->ld_y = d->ld_y;
+    return IFX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ifx_fp8_code_bytes(int32_t rows, int32_t k)
+{
+    return check_fp8(rows, k) == IFX_OK ? (size_t)((k + 127LL) / 128) * rows * 128 : 0;
+}
+
+size_t ifx_fp8_scale_bytes(int32_t rows, int32_t k)
+{
+    return check_fp8(rows, k) == IFX_OK ? (size_t)((k + 511LL) / 512) * rows * 4 : 0;
+}
+
+ifx_status ifx_fp8_quantize(const void *x, int32_t type, int64_t ld, int32_t rows, int32_t k, int32_t format, uint8_t *codes,
+                            uint8_t *scales, void *stream)
+{
+    const ifx_status st = check_fp8_rows(x, type, ld, rows, k, rows, k, format, codes, scales);
+    if (st != IFX_OK || rows == 0) return st;
+    return hip_status(ifx::launch_fp8_quantize(x, type, ld, rows, k, format, codes, scales, (hipStream_t)stream));
+}
+
+ifx_status ifx_fp8_quantize_t(const void *x, int32_t type, int64_t ld, int32_t rows, int32_t k, int32_t format,
+                              uint8_t *codes, uint8_t *scales, void *stream)
+{
+    const ifx_status st = check_fp8_rows(x, type, ld, k, rows, rows, k, format, codes, scales);
+    if (st != IFX_OK || rows == 0) return st;
+    // a workgroup takes one panel of at least 32 rows
+    if (rows > 0x7fffffff - 64 || (k + 127LL) / 128 * ((rows + 31LL) / 32) > 0xffffffffLL / 256) return IFX_E_SHAPE;
+    return hip_status(ifx::launch_fp8_quantize_t(x, type, ld, rows, k, format, codes, scales, (hipStream_t)stream));
+}
+
+ifx_status ifx_fp8_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t format, int32_t rows, int32_t k, void *y,
+                              int32_t type, int64_t ld, void *stream)
+{
+    const ifx_status st = check_fp8_rows(y, type, ld, rows, k, rows, k, format, codes, scales);
+    if (st != IFX_OK || rows == 0) return st;
+    return hip_status(ifx::launch_fp8_dequantize(codes, scales, format, rows, k, y, type, ld, (hipStream_t)stream));
+}
+
+ifx_status ifx_fp8_matmul(const ifx_fp8_desc *d, const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
+                          const uint8_t *w_scales, const float *bias, const void *residual, void *y, void *stream)
+{
+    if (!d) return IFX_E_NULL;
+    if (!known_type(d->type) || !known_act(d->act) || !known_format(d->a_format)) return IFX_E_UNSUPPORTED;
+    ifx_status st = check_product(d->m, d->n, d->k);
+    if (st != IFX_OK) return st;
+    if (!pitch_ok(d->m, d->n, d->ld_y) || (residual && !pitch_ok(d->m, d->n, d->ld_res))) return IFX_E_SHAPE;
+    if (d->m == 0 || d->n == 0) return IFX_OK;
+    if (!y) return IFX_E_NULL;
+    st = check_codes(a_codes, a_scales);
+    if (st == IFX_OK) st = check_codes(w_codes, w_scales);
+    if (st != IFX_OK) return st;
+    const size_t e = type_bytes(d->type);
+    if (!aligned_to(y, e) || !aligned_to(residual, e) || !aligned_to(bias, 4)) return IFX_E_ALIGN;
+    ifx::Fp8Args a = {};
+    a.a_codes = a_codes;
+    a.a_scales = a_scales;
+    a.w_codes = w_codes;
+    a.w_scales = w_scales;
+    a.bias = bias;
+    a.res = residual;
+    a.y = y;
+    a.m = d->m;
+    a.n = d->n;
+    a.k1 = (d->k - 1) / 128 + 1;
+    a.a_format = d->a_format;
+    a.type = d->type;
+    a.act = d->act;
+    a.ld_y = d->ld_y;
+    a.ld_res = d->ld_res;
+    return hip_status(ifx::launch_fp8(a, ifx::kProduct, (hipStream_t)stream));
+}
+
+ifx_status ifx_gated(const ifx_gated_desc *d, const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *g_codes,
+                     const uint8_t *g_scales, const uint8_t *u_codes, const uint8_t *u_scales, void *y, void *stream)
+{
+    const ifx_status st = check_gated(d, x_codes, x_scales, g_codes, g_scales, u_codes, u_scales);
+    if (st != IFX_OK) return st;
+    if (!pitch_ok(d->m, d->n, d->ld_y)) return IFX_E_SHAPE;
+    if (d->m == 0 || d->n == 0) return IFX_OK;
+    if (!y) return IFX_E_NULL;
+    if (!aligned_to(y, type_bytes(d->type))) return IFX_E_ALIGN;
+    ifx::Fp8Args a = gated_args(d, x_codes, x_scales, g_codes, g_scales, u_codes, u_scales);
+    a.y = y;
+    return hip_status(ifx::launch_fp8(a, ifx::kGated, (hipStream_t)stream));
+}
+
+size_t ifx_gated_workspace_bytes(const ifx_gated_desc *d)
+{
+    return d && check_product(d->m, d->n, d->k) == IFX_OK ? gated_workspace(d->m, d->n) : 0;
+}
+
+ifx_status ifx_gated_fp8(const ifx_gated_desc *d, const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *g_codes,
+                         const uint8_t *g_scales, const uint8_t *u_codes, const uint8_t *u_scales, uint8_t *codes,
+                         uint8_t *scales, void *ws, size_t ws_bytes, void *stream)
+{
+    ifx_status st = check_gated(d, x_codes, x_scales, g_codes, g_scales, u_codes, u_scales);
+    if (st != IFX_OK) return st;
+    if (d->m == 0 || d->n == 0) return IFX_OK;
+    st = check_fp8(d->m, d->n);
+    if (st == IFX_OK) st = check_codes(codes, scales);
+    if (st != IFX_OK) return st;
+    if (!aligned16(ws)) return IFX_E_ALIGN;
+    const size_t need = gated_workspace(d->m, d->n);
+    if (need > ws_bytes) return IFX_E_WORKSPACE;
+    if (need > 0 && !ws) return IFX_E_NULL;
+    ifx::Fp8Args a = gated_args(d, x_codes, x_scales, g_codes, g_scales, u_codes, u_scales);
+    a.codes = codes;
+    a.scales = scales;
+    a.ws = (float *)ws;
+    return hip_status(ifx::launch_fp8(a, ifx::kGated, (hipStream_t)stream));
+}
+
+ifx_status ifx_gated_backward(const ifx_gated_desc *d, const void *dy, const uint8_t *x_codes, const uint8_t *x_scales,
+                              const uint8_t *g_codes, const uint8_t *g_scales, const uint8_t *u_codes,
+                              const uint8_t *u_scales, void *dgate, void *dup, void *stream)
+{
+    const ifx_status st = check_gated(d, x_codes, x_scales, g_codes, g_scales, u_codes, u_scales);
+    if (st != IFX_OK) return st;
+    if (!pitch_ok(d->m, d->n, d->ld_y) || !pitch_ok(d->m, d->n, d->ld_up) || !pitch_ok(d->m, d->n, d->ld_dy))
+        return IFX_E_SHAPE;
+    if (d->m == 0 || d->n == 0) return IFX_OK;
+    if (!dy || !dgate || !dup) return IFX_E_NULL;
+    const size_t e = type_bytes(d->type);
+    if (!aligned_to(dy, e) || !aligned_to(dgate, e) || !aligned_to(dup, e)) return IFX_E_ALIGN;
+    ifx::Fp8Args a = gated_args(d, x_codes, x_scales, g_codes, g_scales, u_codes, u_scales);
+    a.res = dy;
+    a.ld_res = d->ld_dy;
+    a.y = dgate;
+    a.y2 = dup;
+    a.ld_y2 = d->ld_up;
+    return hip_status(ifx::launch_fp8(a, ifx::kGatedGrad, (hipStream_t)stream));
+}
+
+ifx_status ifx_rms_norm(const ifx_rms_desc *d, const void *x, const void *residual, const float *weight, void *h, void *y,
+                        float *rstd, void *stream)
+{
+    ifx::RmsArgs a;
+    ifx_status st = check_rms_forward(d, x, residual, weight, h, rstd, &a);
+    if (st != IFX_OK || d->rows == 0) return st;
+    if (!y) return IFX_E_NULL;
+    st = check_operand(d, y, d->ld_y);
+    if (st != IFX_OK) return st;
+    a.y = y;
+    return hip_status(ifx::launch_rms_norm(a, (hipStream_t)stream));
+}
+
+ifx_status ifx_rms_norm_fp8(const ifx_rms_desc *d, const void *x, const void *residual, const float *weight, void *h,
+                            uint8_t *codes, uint8_t *scales, float *rstd, void *stream)
+{
+    ifx::RmsArgs a;
+    ifx_status st = check_rms_forward(d, x, residual, weight, h, rstd, &a);
+    if (st != IFX_OK || d->rows == 0) return st;
+    st = check_codes(codes, scales);
+    if (st != IFX_OK) return st;
+    a.codes = codes;
+    a.scales = scales;
+    return hip_status(ifx::launch_rms_norm(a, (hipStream_t)stream));
+}
+
+size_t ifx_rms_norm_workspace_bytes(const ifx_rms_desc *d)
+{
+    return check_rms(d) == IFX_OK ? ifx::rms_workspace_bytes(d->rows, d->c) : 0;
+}
+
+ifx_status ifx_rms_norm_backward(const ifx_rms_desc *d, const void *dy, const void *h, const float *rstd,
+                                 const float *weight, const void *dh, void *dx, float *dweight, void *ws, size_t ws_bytes,
+                                 void *stream)
+{
+    ifx_status st = check_rms(d);
+    if (st != IFX_OK) return st;
+    if (!aligned_to(dweight, 4)) return IFX_E_ALIGN;
+    ifx::RmsArgs a = {};
+    a.rows = d->rows;
+    a.c = d->c;
+    a.type = d->type;
+    if (d->rows > 0) {
+        if (!dy || !h || !rstd || !dx) return IFX_E_NULL;
+        st = check_operand(d, h, d->ld_x);
+        if (st == IFX_OK) st = check_operand(d, dy, d->ld_dy);
+        if (st == IFX_OK) st = check_operand(d, dx, d->ld_y);
+        if (st == IFX_OK) st = check_operand(d, dh, d->ld_dh);
+        if (st != IFX_OK) return st;
+        if (!aligned_to(weight, 4) || !aligned_to(rstd, 4) || !aligned16(ws)) return IFX_E_ALIGN;
+        const size_t need = dweight ? ifx::rms_workspace_bytes(d->rows, d->c) : 0;
+        if (need > ws_bytes) return IFX_E_WORKSPACE;
+        if (need > 0 && !ws) return IFX_E_NULL;
+        a.x = h;
+        a.dy = dy;
+        a.dh = dh;
+        a.y = dx;
+        a.weight = weight;
+        a.rstd = const_cast<float *>(rstd);
+        a.part = (float *)ws;
+        a.ld_x = d->ld_x;
+        a.ld_y = d->ld_y;
+        a.ld_dy = d->ld_dy;
+        a.ld_dh = d->ld_dh;
+    }
+    return hip_status(ifx::launch_rms_norm_grad(a, dweight, (hipStream_t)stream));
+}
+
+}  // extern "C"

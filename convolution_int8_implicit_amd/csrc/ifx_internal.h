@@ -168,6 +168,38 @@ struct Mx4Args {
     int past;  // set by the launcher: y is stored past the caches (stored_past)
 };
 
+// One product of two 8-bit tensors, or the gated pair of projections and its gradient (device pointers; see
+// ifx_fp8_matmul, ifx_gated, ifx_gated_fp8 and ifx_gated_backward).
+struct Fp8Args {
+    const uint8_t *a_codes, *a_scales;  // [k1][m][128], [ceil(k1 / 4)][m][4]
+    const uint8_t *w_codes, *w_scales;  // [k1][n][128], [ceil(k1 / 4)][n][4]: the weights, or the gate's
+    const uint8_t *u_codes, *u_scales;  // the other projection's (gated forms)
+    const float *bias;                  // [n] or null (product)
+    const void *res;                    // residual or null (product), dy (gradient), of `type`
+    void *y, *y2;                       // result, of `type`; of the gradient: at the gate and at the other projection
+    uint8_t *codes, *scales;            // instead of y: 8-bit codes of n columns (gated form; else null)
+    float *ws;                          // [m][n]: its values for few rows
+    int m, n, k1;
+    int a_format, type, act;
+    long long ld_y, ld_y2, ld_res;
+    int past;  // set by the launcher: y is stored past the caches (stored_past)
+};
+
+// One root mean square norm or its gradient (device pointers; see ifx_rms_norm).
+struct RmsArgs {
+    const void *x, *res;      // forward: input, residual or null
+    const void *dy, *dh;      // gradient: of the norm, past the norm (or null)
+    void *h, *y;              // forward: the sum (or null), the norm (null in the 8-bit form); gradient: x is the sum, y is dx
+    uint8_t *codes, *scales;  // forward: instead of y (else null)
+    const float *weight;      // [c] or null
+    float *rstd;              // [rows]; written by the forward pass (or null), read by the gradient
+    float *part;              // gradient: partial sums of dweight, [chunks][c] (null: no dweight)
+    int rows, c, type;
+    float eps;
+    long long ld_x, ld_res, ld_h, ld_y, ld_dy, ld_dh;
+    int past, chunks;  // set by the launcher
+};
+
 // Whether rows of a result are stored past the caches: they begin on 128-byte lines, so that stores fill whole
 // lines, and there are more bytes than would stay in the L2s (4 MB in each of eight) until they are read.
 // us, cached / past: product 100352 x 128 x 512 14.9 / 11.8, 50176 x 512 x 128 17.2 / 15.5, 4096^3 39.8 / 37.7;
@@ -229,6 +261,22 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
                                  long long ld, hipStream_t s);
 hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s);
 hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s);  // its tiled form, mx4_gemm.hip
+// 8-bit rounding, values and products, fp8.hip; the tiled forms, fp8_gemm.hip
+hipError_t launch_fp8_quantize(const void *x, int type, long long ld, int rows, int k, int format, uint8_t *codes,
+                               uint8_t *scales, hipStream_t s);
+hipError_t launch_fp8_quantize_t(const void *x, int type, long long ld, int rows, int k, int format, uint8_t *codes,
+                                 uint8_t *scales, hipStream_t s);
+hipError_t launch_fp8_dequantize(const uint8_t *codes, const uint8_t *scales, int format, int rows, int k, void *y,
+                                 int type, long long ld, hipStream_t s);
+enum Fp8Mode { kProduct, kGated, kGatedGrad };
+// Whether a launch of these sizes takes the few-rows form (whose 8-bit results pass through Fp8Args::ws).
+bool fp8_few_rows(int m, int n);
+hipError_t launch_fp8(Fp8Args a, Fp8Mode mode, hipStream_t s);
+hipError_t launch_fp8_tiles(Fp8Args a, Fp8Mode mode, hipStream_t s);
+// root mean square norm and its gradient, rms.hip
+size_t rms_workspace_bytes(int rows, int c);
+hipError_t launch_rms_norm(RmsArgs a, hipStream_t s);
+hipError_t launch_rms_norm_grad(RmsArgs a, float *dweight, hipStream_t s);
 // group norm with an activation and its gradient, norm.hip
 bool gn_supported(int n, int hw, int c, int groups);
 size_t gn_workspace_bytes(int n, int hw, int c, int groups, int type, bool grad, bool mx4);

@@ -1,6 +1,6 @@
-// Device helpers of the 4-bit and normalisation kernels: typed loads and stores of eight
-// consecutive values, the activation functions and the rounding of a block of 32 values to
-// microscaled 4-bit codes.
+// Device helpers of the 4-bit, 8-bit and normalisation kernels: typed loads and stores of eight
+// consecutive values, the activation functions, the rounding of a block of 32 values to
+// microscaled 4-bit codes and of one of 128 to 8-bit codes.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -138,6 +138,47 @@ __device__ __forceinline__ void store8(E *p, int valid, const float (&f)[8])
     }
 }
 
+// Four consecutive values at any element boundary.
+template <typename E>
+struct Quad {
+    E v[4];
+};
+
+// One value of a type known at run time.
+__device__ __forceinline__ float load_any(const void *p, int type, long long i)
+{
+    return type == 0 ? ((const float *)p)[i] : type == 1 ? (float)((const __bf16 *)p)[i] : (float)((const _Float16 *)p)[i];
+}
+__device__ __forceinline__ void store_any(void *p, int type, long long i, float f)
+{
+    if (type == 0)
+        ((float *)p)[i] = f;
+    else if (type == 1)
+        ((__bf16 *)p)[i] = (__bf16)f;
+    else
+        ((_Float16 *)p)[i] = (_Float16)f;
+}
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// f(Int<0>()) .. f(Int<N - 1>())
+template <int I, int N, typename F>
+__device__ __forceinline__ void each_from(F &f)
+{
+    if constexpr (I < N) {
+        f(Int<I>());
+        each_from<I + 1, N>(f);
+    }
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(Int<N>, F f)
+{
+    each_from<0, N>(f);
+}
+
 // Activations (include/ifx.h: IFX_ACT_NONE, IFX_ACT_RELU, IFX_ACT_SILU).  A NaN stays a NaN.  The
 // sigmoid is one exponential and one reciprocal instruction, each good to a unit in the last place.
 __device__ __forceinline__ float sigmoid(float z)
@@ -167,6 +208,18 @@ __device__ __forceinline__ float act_of(float z)
     return z;
 }
 
+// The derivative of an activation, for a ReLU 0 where z <= 0.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z)
+{
+    if (ACT == 1) return z > 0.0f ? 1.0f : 0.0f;
+    if (ACT == 2) {
+        const float s = sigmoid(z);
+        return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    return 1.0f;
+}
+
 // f(tag) with the activation as a compile-time constant, so no value's loop chooses one.
 template <typename F>
 __device__ __forceinline__ void with_act(int act, F f)
@@ -177,6 +230,30 @@ __device__ __forceinline__ void with_act(int act, F f)
         f(Slot1());
     else
         f(Slot0());
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v)
+{
+    return v + __uint_as_float((unsigned)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over the 2^k = `lanes` (at most 64) neighbouring lanes, in every one of them.
+__device__ __forceinline__ float lanes_sum(float v, int lanes)
+{
+    if (lanes > 1) v = dpp_add<0xb1>(v);   // lanes 1 0 3 2
+    if (lanes > 2) v = dpp_add<0x4e>(v);   // lanes 2 3 0 1
+    if (lanes > 4) v = dpp_add<0x141>(v);  // eight lanes reversed
+    if (lanes > 8) v = dpp_add<0x140>(v);  // sixteen lanes reversed
+    if (lanes > 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if (lanes > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
 }
 
 // Maximum over the four lanes 4i .. 4i + 3 (every lane of the wave active).
@@ -209,6 +286,87 @@ __device__ __forceinline__ unsigned mx4_codes(const float (&f)[8], unsigned &sca
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[4], f[5], sf, 2);
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[6], f[7], sf, 3);
     return bad ? 0u : r;
+}
+
+// Maximum over the sixteen lanes 16i .. 16i + 15 (every lane of the wave active).
+__device__ __forceinline__ unsigned row_max(unsigned u)
+{
+    u = quad_max(u);
+    u = max(u, (unsigned)__builtin_amdgcn_mov_dpp((int)u, 0x141, 0xf, 0xf, true));  // mirrored in eight lanes
+    return max(u, (unsigned)__builtin_amdgcn_mov_dpp((int)u, 0x140, 0xf, 0xf, true));  // mirrored in sixteen
+}
+
+// The largest of eight magnitudes as a bit pattern, above which only NaNs and infinities lie.
+__device__ __forceinline__ unsigned top_bits(const float (&f)[8])
+{
+    float top = __builtin_elementwise_maximum(fabsf(f[0]), fabsf(f[1]));
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, fabsf(f[2])), fabsf(f[3]));
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, fabsf(f[4])), fabsf(f[5]));
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, fabsf(f[6])), fabsf(f[7]));
+    return __float_as_uint(top) & 0x7fffffffu;
+}
+
+// 8-bit floating point (include/ifx.h: IFX_FP8_E4M3 is 0, IFX_FP8_E5M2 is 1).  The scale byte of a block whose
+// largest magnitude has the bit pattern u: both formats' largest value is 1.75 times a power of two (448 and
+// 57344), so the smallest power of two under which the block fits follows from u's exponent and whether its
+// mantissa passes 1.75.  255 for a NaN or an infinity.
+template <int FMT>
+__device__ __forceinline__ unsigned fp8_scale(unsigned u)
+{
+    constexpr unsigned T = FMT ? 15u : 8u;
+    const unsigned e = (u + 0x1fffffu) >> 23;
+    return u >= 0x7f800000u ? 255u : max(e, T) - T;
+}
+
+typedef short fp8_v2s __attribute__((ext_vector_type(2)));
+
+// Eight codes of a block with scale byte s, in two words, the lowest column in the lowest byte.  The
+// conversion rounds x / 2^(s - 127) to nearest even; the scale leaves nothing to saturate.
+template <int FMT>
+__device__ __forceinline__ uint2 fp8_codes(const float (&f)[8], unsigned s)
+{
+    const float sf = __uint_as_float((s > 254u ? 0u : s) << 23);  // the instruction reads the exponent field only
+    fp8_v2s lo = {0, 0}, hi = {0, 0};
+    if constexpr (FMT) {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(lo, f[0], f[1], sf, false);
+        lo = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(lo, f[2], f[3], sf, true);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(hi, f[4], f[5], sf, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(hi, f[6], f[7], sf, true);
+    } else {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, f[0], f[1], sf, false);
+        lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, f[2], f[3], sf, true);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, f[4], f[5], sf, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, f[6], f[7], sf, true);
+    }
+    const bool bad = s > 254u;
+    return make_uint2(bad ? 0u : __builtin_bit_cast(unsigned, lo), bad ? 0u : __builtin_bit_cast(unsigned, hi));
+}
+
+typedef __bf16 lowp_v8b __attribute__((ext_vector_type(8)));
+
+// 32 codes times their block's power of two, in four vectors of bfloat16.  Exact from scale byte 10 on (e4m3; 17 for
+// e5m2), below which the smallest codes pass the smallest normal bfloat16.
+template <int FMT>
+__device__ __forceinline__ void fp8_widen(ifx_v4i lo, ifx_v4i hi, unsigned s, lowp_v8b (&out)[4])
+{
+    const float sf = __uint_as_float((s & 255u) << 23);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+            const int t = 2 * q + h;
+            const unsigned w = (unsigned)(t < 4 ? lo[t & 3] : hi[t & 3]);
+            v2b a, b;
+            if constexpr (FMT) {
+                a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, sf, false);
+                b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, sf, true);
+            } else {
+                a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sf, false);
+                b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sf, true);
+            }
+            out[q][4 * h] = a[0], out[q][4 * h + 1] = a[1], out[q][4 * h + 2] = b[0], out[q][4 * h + 3] = b[1];
+        }
 }
 
 }  // namespace ifx

@@ -112,20 +112,6 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *code
 // ------------------------------------------------------------------------------------------
 // Product y[m, n] = act(sum_k A[m, k] W[n, k] + bias[n] + residual[m, n]).
 // ------------------------------------------------------------------------------------------
-__device__ __forceinline__ float load_any(const void *p, int type, long long i)
-{
-    return type == 0 ? ((const float *)p)[i] : type == 1 ? (float)((const __bf16 *)p)[i] : (float)((const _Float16 *)p)[i];
-}
-__device__ __forceinline__ void store_any(void *p, int type, long long i, float f)
-{
-    if (type == 0)
-        ((float *)p)[i] = f;
-    else if (type == 1)
-        ((__bf16 *)p)[i] = (__bf16)f;
-    else
-        ((_Float16 *)p)[i] = (_Float16)f;
-}
-
 // Few rows: a workgroup of kRowWaves waves takes 16 weight rows and 16 MT rows of A; wave w multiplies
 // panels w, w + kRowWaves, ... straight from memory (16 rows of a panel are one contiguous kilobyte,
 // one 16-byte load per lane), kAhead of them requested at once, and the partial sums meet in LDS,

@@ -34,32 +34,6 @@ constexpr int kFp4 = 4;  // the matrix instruction's operand format: 4-bit e2m1
 
 __device__ __forceinline__ v8i wide(v4i x) { return (v8i){x[0], x[1], x[2], x[3], 0, 0, 0, 0}; }
 
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
-
-// f(Int<0>()) .. f(Int<N - 1>())
-template <int I, int N, typename F>
-__device__ __forceinline__ void each_from(F &f)
-{
-    if constexpr (I < N) {
-        f(Int<I>());
-        each_from<I + 1, N>(f);
-    }
-}
-template <int N, typename F>
-__device__ __forceinline__ void each(Int<N>, F f)
-{
-    each_from<0, N>(f);
-}
-
-// Four consecutive output values at any element boundary.
-template <typename E>
-struct Quad {
-    E v[4];
-};
-
 template <int BM_, int BN_, int WM_, int WN_, int ST_>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;

@@ -139,30 +139,6 @@ struct Pixels {
     __device__ __forceinline__ void advance(int i) { at += i * stride; }
 };
 
-template <int CTRL>
-__device__ __forceinline__ float dpp_add(float v)
-{
-    return v + __uint_as_float((unsigned)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
-}
-
-// Sum over the 2^k = `lanes` (at most 64) neighbouring lanes, in every one of them.
-__device__ __forceinline__ float lanes_sum(float v, int lanes)
-{
-    if (lanes > 1) v = dpp_add<0xb1>(v);   // lanes 1 0 3 2
-    if (lanes > 2) v = dpp_add<0x4e>(v);   // lanes 2 3 0 1
-    if (lanes > 4) v = dpp_add<0x141>(v);  // eight lanes reversed
-    if (lanes > 8) v = dpp_add<0x140>(v);  // sixteen lanes reversed
-    if (lanes > 16) {
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    }
-    if (lanes > 32) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    }
-    return v;
-}
-
 // Per-group values of the thread's eight channels.  VEC: cg is a multiple of 8, so they are one group's
 // and one register serves all eight.
 template <bool VEC>

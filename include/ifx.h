@@ -28,7 +28,7 @@
  *     an error status nothing has been enqueued.  Validation touches no
  *     device, so every error path runs without a GPU.
  *   - All arithmetic of the int8 path is integer; results are deterministic
- *     and bit-exact.  The 4-bit and group norm entry points at the end of this
+ *     and bit-exact.  The 4-bit, 8-bit and norm entry points at the end of this
  *     file compute in 32-bit floating point; they too are deterministic.
  *
  * Layouts (Inspur conv-merge article, section 3.1):
@@ -454,7 +454,7 @@ ifx_status ifx_quantize_u8(const uint8_t *x, int8_t *q, int64_t count, int32_t c
  */
 ifx_status ifx_dequantize_i32(const int32_t *q, float *y, int64_t count, float scale, void *stream);
 
-/* Element types and activations of the 4-bit and group norm entry points. */
+/* Element types and activations of the 4-bit, 8-bit and norm entry points. */
 enum { IFX_F32 = 0, IFX_BF16 = 1, IFX_F16 = 2 };
 enum { IFX_ACT_NONE = 0, IFX_ACT_RELU = 1, IFX_ACT_SILU = 2 }; /* z, max(z, 0), z / (1 + e^-z) */
 
@@ -578,6 +578,169 @@ ifx_status ifx_group_norm_backward(const ifx_gn_desc *d, const void *dy, const v
  * ifx_group_norm_mx4 (form 2) launches for d with n >= 1, as ifx_conv_kernel_name below answers for a convolution.
  */
 ifx_status ifx_group_norm_kernel_name(const ifx_gn_desc *d, int32_t form, char *buf, size_t len);
+
+/* The 8-bit floating point formats: sign, 4 exponent and 3 mantissa bits, up to 448, without infinities; sign, 5
+   exponent and 2 mantissa bits, up to 57344. */
+enum { IFX_FP8_E4M3 = 0, IFX_FP8_E5M2 = 1 };
+
+/*
+ * 8-bit floating point with a power of two for each block of 128.  A tensor of
+ * `rows` rows and k columns holds blocks of 128 consecutive columns of a row:
+ * a byte per column and one byte s per block; a column's value is
+ * code * 2^(s - 127), NaN where s is 255.  Layout, K1 = ceil(k / 128):
+ *   codes   [K1, rows, 128] uint8: column 128 i + j at [i, row, j]
+ *   scales  [ceil(K1 / 4), rows, 4] uint8: the block of columns 128 i .. at
+ *           [i / 4, row, i % 4]
+ * Codes of columns past k are 0 (so are a word's scales past the last block);
+ * the products rely on the codes.
+ *
+ * ifx_fp8_quantize rounds a block x to it:
+ *   s    = the smallest byte with max |x| <= M 2^(s - 127), M the format's
+ *          largest value (448 or 57344), at least 0 (0 for a block of zeros)
+ *   code = x / 2^(s - 127) rounded to the nearest value, halves to the even code
+ * so nothing saturates.  A block that holds a NaN or an infinity gets s = 255
+ * and zero codes.  ifx_fp8_quantize_t rounds the transpose: x has k rows of
+ * `rows` elements, one every ld >= rows, and the result's row r is x's column
+ * r, its blocks 128 consecutive rows of x (the operands of a weight's
+ * gradient dy^T x).  ifx_fp8_dequantize writes the values, rounded once where
+ * `type` does not hold them.
+ *   x, y    DEVICE, of `type`, aligned to the element
+ *   codes   DEVICE, ifx_fp8_code_bytes, 16-byte aligned
+ *   scales  DEVICE, ifx_fp8_scale_bytes, 4-byte aligned
+ *   rows    >= 0 (0: nothing to do, pointers are not looked at); k >= 1; at
+ *           most 2^32 / 256 tiles of 16 rows and 512 columns (transposed also:
+ *           of 32 rows and 128 columns, and rows <= 2^31 - 65)
+ * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN and
+ * IFX_E_UNSUPPORTED for an unknown type or format.
+ */
+size_t ifx_fp8_code_bytes(int32_t rows, int32_t k);  /* host-only; 0 for a bad shape */
+size_t ifx_fp8_scale_bytes(int32_t rows, int32_t k); /* host-only; 0 for a bad shape */
+
+ifx_status ifx_fp8_quantize(const void *x, int32_t type, int64_t ld, int32_t rows, int32_t k, int32_t format,
+                            uint8_t *codes, uint8_t *scales, void *stream);
+ifx_status ifx_fp8_quantize_t(const void *x, int32_t type, int64_t ld, int32_t rows, int32_t k, int32_t format,
+                              uint8_t *codes, uint8_t *scales, void *stream);
+ifx_status ifx_fp8_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t format, int32_t rows, int32_t k,
+                              void *y, int32_t type, int64_t ld, void *stream);
+
+/*
+ * Product of two such tensors, A of m rows (either format) and W of n rows
+ * (e4m3), both of k columns:
+ *   y[i, j] = act(sum_c A[i, c] W[j, c] + bias[j] + residual[i, j])
+ * accumulated in 32-bit floating point and rounded once to `type`.  Results of
+ * 16 bits (and 8, below) are computed on the 8-bit matrix units, which cut each
+ * of the eight products that they add at a time off below 2^-13 of the largest:
+ * 1.5e-5 of a result on normally distributed values, at most 7 2^-13 of the sum
+ * of its terms' magnitudes.  IFX_F32 results are computed on the 16-bit ones, in
+ * full precision at half the rate; there, codes whose value lies below the
+ * smallest normal bfloat16 (possible where s < 10, in e5m2 s < 17) may count as
+ * zero.  The sum of one (m, n, k) and type is taken in one order, so results
+ * are the same from call to call.  A NaN block makes its row of y (A) or its
+ * column (W) NaN.
+ *   bias      DEVICE float32 [n], 4-byte aligned, or NULL
+ *   residual  DEVICE, m rows of n elements of `type`, one every ld_res >= n
+ *             elements, element-aligned, or NULL; may be y itself (same pitch)
+ *   y         DEVICE, m rows of n elements of `type`, one every ld_y >= n
+ *             elements, element-aligned; no other operand may overlap it
+ *   m, n      >= 0 (either 0: nothing to do), at most 2^24 - 9 tiles of 64 x 64; k >= 1
+ * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN,
+ * IFX_E_UNSUPPORTED (type, act, format).
+ */
+typedef struct {
+    int32_t m, n, k;
+    int32_t a_format;
+    int32_t type, act;
+    int64_t ld_y, ld_res;
+} ifx_fp8_desc;
+
+ifx_status ifx_fp8_matmul(const ifx_fp8_desc *d, const uint8_t *a_codes, const uint8_t *a_scales,
+                          const uint8_t *w_codes, const uint8_t *w_scales, const float *bias, const void *residual,
+                          void *y, void *stream);
+
+/*
+ * The gated pair of projections of a feed-forward layer, X of m rows, G and U
+ * of n rows, all e4m3 of k columns:
+ *   gate = X G^T, up = X U^T, y = act(gate) * up
+ * Sums are taken as ifx_fp8_matmul's and held in 32 bits as y is; ifx_gated rounds y once
+ * to `type`, ifx_gated_fp8 to e4m3 codes of m rows and n columns (the operand
+ * of the projection back).  ifx_gated_backward takes the gradient dy of y,
+ * recomputes both projections and writes
+ *   dgate = dy * up * act'(gate) (for ReLU 0 where gate <= 0),  dup = dy * act(gate)
+ * to `type`, from which the products with G, U and X give the gradients of X,
+ * G and U (ifx_fp8_quantize, ifx_fp8_quantize_t, ifx_fp8_matmul).
+ *   y, dy, dgate, dup  DEVICE, m rows of n elements of `type`, element-aligned,
+ *                      pitches ld_y (y, dgate), ld_up (dup) and ld_dy >= n;
+ *                      dgate or dup may be dy (same pitch), nothing else may overlap
+ *   ws                 DEVICE, 16-byte aligned, at least
+ *                      ifx_gated_workspace_bytes (may be NULL where that is 0)
+ *   m, n               >= 0 (either 0: nothing to do), at most 2^24 - 9 tiles of 64 x 64; k >= 1
+ * Pitches of a call's absent operands are not looked at.
+ * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE, IFX_E_ALIGN,
+ * IFX_E_WORKSPACE, IFX_E_UNSUPPORTED (type, act).
+ */
+typedef struct {
+    int32_t m, n, k;
+    int32_t type, act;
+    int64_t ld_y, ld_up, ld_dy;
+} ifx_gated_desc;
+
+size_t ifx_gated_workspace_bytes(const ifx_gated_desc *d); /* host-only, of ifx_gated_fp8; 0 for a bad desc */
+
+ifx_status ifx_gated(const ifx_gated_desc *d, const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *g_codes,
+                     const uint8_t *g_scales, const uint8_t *u_codes, const uint8_t *u_scales, void *y, void *stream);
+ifx_status ifx_gated_fp8(const ifx_gated_desc *d, const uint8_t *x_codes, const uint8_t *x_scales,
+                         const uint8_t *g_codes, const uint8_t *g_scales, const uint8_t *u_codes,
+                         const uint8_t *u_scales, uint8_t *codes, uint8_t *scales, void *ws, size_t ws_bytes,
+                         void *stream);
+ifx_status ifx_gated_backward(const ifx_gated_desc *d, const void *dy, const uint8_t *x_codes, const uint8_t *x_scales,
+                              const uint8_t *g_codes, const uint8_t *g_scales, const uint8_t *u_codes,
+                              const uint8_t *u_scales, void *dgate, void *dup, void *stream);
+
+/*
+ * Root mean square norm over `rows` rows of c elements, with the addition of
+ * the residual:
+ *   h = x + residual, rounded to `type` as it is kept (x without a residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
+ * ifx_rms_norm rounds y once to `type`; ifx_rms_norm_fp8 rounds the same 32-bit
+ * values to e4m3 codes of `rows` rows and c columns (ifx_fp8_quantize).  Both
+ * write h and rstd where the pointers are not NULL.  With the gradient dy of y
+ * and dh of h (what reaches the sum past the norm, or NULL), d = dy * weight
+ * and xhat = h * rstd, ifx_rms_norm_backward writes
+ *   dx = dh + rstd * (d - xhat * mean(d * xhat))   (to `type`; x's and the residual's)
+ *   dweight = sum over rows of dy * xhat            (where the pointer is not NULL)
+ * from the forward pass's h and rstd.
+ *   x, residual, h, y, dy, dh, dx  DEVICE, of `type`, element-aligned, pitches
+ *           ld_x (x; the gradient's h), ld_res, ld_h, ld_y (y, dx), ld_dy and
+ *           ld_dh >= c; an absent operand's is not looked at.  h may be x or
+ *           the residual, y may be x, the residual or neither, not h; dx may be
+ *           dy, h or dh (same pitches)
+ *   weight  DEVICE float32 [c], 4-byte aligned, or NULL (1)
+ *   dweight, rstd  DEVICE float32 [c] and [rows], 4-byte aligned
+ *   rows    >= 0 (0: only dweight is written, zeros); 1 <= c <= 24576; eps >= 0.
+ *           Squares are summed in 32 bits: with eps = 0 a row's root mean square
+ *           has to be at least 2^-60
+ *   ws      DEVICE, 16-byte aligned, at least ifx_rms_norm_workspace_bytes (may
+ *           be NULL where that is 0 or dweight is NULL)
+ * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE (also more rows than a
+ * launch of 2^32 work-items holds), IFX_E_ALIGN, IFX_E_WORKSPACE,
+ * IFX_E_UNSUPPORTED (type, c > 24576).
+ */
+typedef struct {
+    int32_t rows, c;
+    int32_t type;
+    float eps;
+    int64_t ld_x, ld_res, ld_h, ld_y, ld_dy, ld_dh;
+} ifx_rms_desc;
+
+size_t ifx_rms_norm_workspace_bytes(const ifx_rms_desc *d); /* host-only, of the gradient; 0 for a bad desc */
+
+ifx_status ifx_rms_norm(const ifx_rms_desc *d, const void *x, const void *residual, const float *weight, void *h,
+                        void *y, float *rstd, void *stream);
+ifx_status ifx_rms_norm_fp8(const ifx_rms_desc *d, const void *x, const void *residual, const float *weight, void *h,
+                            uint8_t *codes, uint8_t *scales, float *rstd, void *stream);
+ifx_status ifx_rms_norm_backward(const ifx_rms_desc *d, const void *dy, const void *h, const float *rstd,
+                                 const float *weight, const void *dh, void *dx, float *dweight, void *ws,
+                                 size_t ws_bytes, void *stream);
 
 /*
  * Host-only: the kernel instance ifx_conv_fused(d, ...) launches, named as
