@@ -307,95 +307,147 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
         constexpr int TO = TWO ? C::TN / 2 : C::TN;  // columns of the wave's results
         int8_t *out = smem + w * 32 * C::ROW;
         constexpr int LPR = TO / 4, RPP = 64 / LPR, P = 32 / RPP;  // lanes per row, rows per pass, passes
-        const int col = n0 + wn * TO + (el % LPR) * 4, left = a.n - col;
-        const bool whole = left >= 4;  // all of the lane's columns exist
+        // the wave's first row and column, the lane's place in a pass
+        const int r0 = m0 + wm * C::TM, c0 = n0 + wn * TO, lr = el / LPR, lc = el % LPR * 4;
+        const int8_t *const src = out + lr * C::ROW + lc * 4;
+        const int col = c0 + lc, left = a.n - col;
         float bias[4] = {};
         if constexpr (!TWO) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bias[e] = a.bias && whole ? a.bias[col + e] : 0.0f;
+            for (int e = 0; e < 4; ++e) bias[e] = a.bias && left >= 4 ? a.bias[col + e] : 0.0f;
         }
-        with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+        // 32 rows of accumulators staged
+        auto stage = [&](auto act, int i) __attribute__((always_inline)) {
+            if constexpr (FORM == kFormGated) {
+#pragma unroll
+                for (int jj = 0; jj < C::FN / 2; ++jj)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        *(float *)(out + value_row(e) * C::ROW + (jj * 32 + (el & 31)) * 4) = combine(act, i, jj, e);
+            } else {
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) *(float *)(out + value_row(e) * C::ROW + (j * 32 + (el & 31)) * 4) = acc[i][j][e];
+            }
+            wave_lds_sync();
+        };
+        // One result (of the gradient the first of two, `second` the other) from the staged value, the other
+        // projection's and the operand that is read beside them.
+        const auto first = [](auto act, float v, float u, float r) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act)::value;
-            // one result (or two: the gradient's) of staged value v, the other projection's u and the operand r
-            const auto first = [&](float v, float u, float r) __attribute__((always_inline)) {
-                return FORM == kFormProduct ? act_of<ACT>(v + r) : FORM == kFormGated ? v : r * u * act_slope<ACT>(v);
+            return FORM == kFormProduct ? act_of<ACT>(v + r) : FORM == kFormGated ? v : r * u * act_slope<ACT>(v);
+        };
+        const auto second = [](auto act, float v, float r) __attribute__((always_inline)) {
+            return r * act_of<decltype(act)::value>(v);
+        };
+        typedef unsigned QuadWords __attribute__((ext_vector_type(sizeof(E)), aligned(sizeof(E))));
+        // A tile that lies whole in the result: addresses are a uniform base and the lane's offset, nothing is
+        // predicated.  RES: an operand is read.
+        auto whole = [&](auto act, auto res_tag, auto past) __attribute__((always_inline)) {
+            constexpr bool RES = decltype(res_tag)::value;
+            const unsigned off = (unsigned)((lr * (int)a.ld_y + lc) * (int)sizeof(E));
+            const unsigned off2 = FORM == kFormGrad ? (unsigned)((lr * (int)a.ld_y2 + lc) * (int)sizeof(E)) : 0u;
+            const unsigned off_r = RES ? (unsigned)((lr * (int)a.ld_res + lc) * (int)sizeof(E)) : 0u;
+            const auto put = [&](void *y, long long ld, int row, unsigned o, Quad<E> v) __attribute__((always_inline)) {
+                char *const base = (char *)y + (row * ld + c0) * (long long)sizeof(E);
+                if constexpr (decltype(past)::value) {
+                    __builtin_nontemporal_store(__builtin_bit_cast(QuadWords, v), (QuadWords *)(base + o));
+                    keep_apart();
+                } else {
+                    *(Quad<E> *)(base + o) = v;
+                }
             };
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
-                const int r0 = m0 + wm * C::TM + i * 32;
-                if (r0 >= a.m) break;
-                const long long row0 = r0 + el / LPR;
-                // requested before the rows are staged
+                const int row = r0 + i * 32;
+                Quad<E> res[P];
+                if constexpr (RES) {  // requested before the rows are staged
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        res[p] = *(const Quad<E> *)((const char *)a.res + ((row + p * RPP) * a.ld_res + c0) * (long long)sizeof(E) + off_r);
+                }
+                stage(act, i);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const v4f f = *(const v4f *)(src + p * RPP * C::ROW);
+                    v4f u = {};
+                    if constexpr (FORM == kFormGrad) u = *(const v4f *)(src + p * RPP * C::ROW + TO * 4);
+                    Quad<E> q, q2;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float r = RES ? (float)res[p].v[e] : 0.0f, v = FORM == kFormProduct ? f[e] + bias[e] : f[e];
+                        q.v[e] = (E)(RES || FORM != kFormProduct ? first(act, v, u[e], r) : act_of<decltype(act)::value>(v));
+                        if constexpr (FORM == kFormGrad) q2.v[e] = (E)second(act, v, r);
+                    }
+                    put(a.y, a.ld_y, row + p * RPP, off, q);
+                    if constexpr (FORM == kFormGrad) put(a.y2, a.ld_y2, row + p * RPP, off2, q2);
+                }
+                wave_lds_sync();
+            }
+        };
+        // A tile that ends inside: rows predicated by lane, the last one to three columns value by value.
+        auto ragged = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                if (r0 + i * 32 >= a.m) break;
+                const long long row0 = r0 + i * 32 + lr;
                 Quad<E> res[P];
                 if (a.res) {
 #pragma unroll
                     for (int p = 0; p < P; ++p)
-                        if (whole && row0 + p * RPP < a.m) res[p] = *(const Quad<E> *)((const E *)a.res + (row0 + p * RPP) * a.ld_res + col);
+                        if (left >= 4 && row0 + p * RPP < a.m) res[p] = *(const Quad<E> *)((const E *)a.res + (row0 + p * RPP) * a.ld_res + col);
                 }
-                if constexpr (FORM == kFormGated) {
+                stage(act, i);
 #pragma unroll
-                    for (int jj = 0; jj < C::FN / 2; ++jj)
+                for (int p = 0; p < P; ++p) {
+                    if (left < 4 || row0 + p * RPP >= a.m) continue;
+                    const v4f f = *(const v4f *)(src + p * RPP * C::ROW);
+                    v4f u = {};
+                    if constexpr (FORM == kFormGrad) u = *(const v4f *)(src + p * RPP * C::ROW + TO * 4);
+                    Quad<E> q, q2;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            *(float *)(out + value_row(e) * C::ROW + (jj * 32 + (el & 31)) * 4) = combine(act, i, jj, e);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) *(float *)(out + value_row(e) * C::ROW + (j * 32 + (el & 31)) * 4) = acc[i][j][e];
-                }
-                wave_lds_sync();
-                auto rows = [&](auto past) __attribute__((always_inline)) {
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const int8_t *src = out + (p * RPP + el / LPR) * C::ROW + (el % LPR) * 16;
-                        const v4f f = *(const v4f *)src;
-                        v4f u = {};
-                        if constexpr (FORM == kFormGrad) u = *(const v4f *)(src + TO * 4);
-                        Quad<E> q, q2;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float r = a.res ? (float)res[p].v[e] : 0.0f;
-                            q.v[e] = (E)first(FORM == kFormProduct ? f[e] + bias[e] : f[e], u[e], r);
-                            if constexpr (FORM == kFormGrad) q2.v[e] = (E)(r * act_of<ACT>(f[e]));
-                        }
-                        if (!whole || row0 + p * RPP >= a.m) continue;
-                        const auto put = [&](void *y, long long ld, Quad<E> v) __attribute__((always_inline)) {
-                            E *const dst = (E *)y + (row0 + p * RPP) * ld + col;
-                            if constexpr (decltype(past)::value) {
-                                typedef unsigned Words __attribute__((ext_vector_type(sizeof(E)), aligned(sizeof(E))));
-                                __builtin_nontemporal_store(__builtin_bit_cast(Words, v), (Words *)dst);
-                                keep_apart();
-                            } else {
-                                *(Quad<E> *)dst = v;
-                            }
-                        };
-                        put(a.y, a.ld_y, q);
-                        if constexpr (FORM == kFormGrad) put(a.y2, a.ld_y2, q2);
+                    for (int e = 0; e < 4; ++e) {
+                        const float r = a.res ? (float)res[p].v[e] : 0.0f, v = FORM == kFormProduct ? f[e] + bias[e] : f[e];
+                        q.v[e] = (E)first(act, v, u[e], r);
+                        if constexpr (FORM == kFormGrad) q2.v[e] = (E)second(act, v, r);
                     }
-                };
-                if (a.past)
-                    rows(std::true_type());
-                else
-                    rows(std::false_type());
-                if (left > 0 && !whole) {  // the last one to three columns, value by value
+                    *(Quad<E> *)((E *)a.y + (row0 + p * RPP) * a.ld_y + col) = q;
+                    if constexpr (FORM == kFormGrad) *(Quad<E> *)((E *)a.y2 + (row0 + p * RPP) * a.ld_y2 + col) = q2;
+                }
+                if (left > 0 && left < 4) {
 #pragma unroll 1
                     for (int k = 0; k < P * left; ++k) {
                         const int p = k / left, e = k - p * left;
                         const long long row = row0 + p * RPP;
                         if (row >= a.m) break;
-                        const int8_t *src = out + (p * RPP + el / LPR) * C::ROW + (el % LPR) * 16 + e * 4;
-                        float v = *(const float *)src, u = 0.0f, r = 0.0f;
-                        if constexpr (FORM == kFormGrad) u = *(const float *)(src + TO * 4);
-                        if constexpr (FORM == kFormProduct)
+                        float v = *(const float *)(src + p * RPP * C::ROW + e * 4), u = 0.0f, r = 0.0f;
+                        if constexpr (FORM == kFormGrad) u = *(const float *)(src + p * RPP * C::ROW + TO * 4 + e * 4);
+                        if constexpr (!TWO)
                             if (a.bias) v += a.bias[col + e];
                         if (a.res) r = (float)((const E *)a.res)[row * a.ld_res + col + e];
-                        ((E *)a.y)[row * a.ld_y + col + e] = (E)first(v, u, r);
-                        if constexpr (FORM == kFormGrad) ((E *)a.y2)[row * a.ld_y2 + col + e] = (E)(r * act_of<ACT>(v));
+                        ((E *)a.y)[row * a.ld_y + col + e] = (E)first(act, v, u, r);
+                        if constexpr (FORM == kFormGrad) ((E *)a.y2)[row * a.ld_y2 + col + e] = (E)second(act, v, r);
                     }
                 }
                 wave_lds_sync();
             }
+        };
+        const long long most = 1LL << 24;  // pitches whose offsets within a pass fit 32 bits
+        const bool inside = m0 + C::BM <= a.m && n0 + NB <= a.n && a.ld_y <= most && a.ld_y2 <= most && a.ld_res <= most;
+        with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+            auto with_past = [&](auto res_tag) __attribute__((always_inline)) {
+                if (a.past)
+                    whole(act, res_tag, std::true_type());
+                else
+                    whole(act, res_tag, std::false_type());
+            };
+            if (!inside)
+                ragged(act);
+            else if (FORM == kFormGrad || (FORM == kFormProduct && a.res))
+                with_past(std::integral_constant<bool, FORM != kFormGated>());
+            else if constexpr (FORM != kFormGrad)
+                with_past(std::false_type());
         });
     }
 }
