@@ -211,9 +211,11 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(const uint8_t *code
 // ------------------------------------------------------------------------------------------
 // Few rows: y = act(A W^T + bias + residual), act(A G^T) (A U^T), or the latter's gradient at both projections.
 //
-// A workgroup of kRowWaves waves takes 16 weight rows (of both weights in the gated forms) and 16 MT rows of A; its
-// waves take panels in turn straight from memory, several requested at once, and the partial sums meet in LDS,
-// added in wave order.  What bounds it: the weights, read once for MT = 1.
+// For up to 16 rows of A.  A workgroup of kRowWaves waves takes 16 weight rows (of both weights in the gated forms); its
+// waves take panels in turn straight from memory, several requested at once, and the partial sums meet in LDS, added in
+// wave order.  What bounds it: the weights, read once (one row of 8192 x 8192, launch included, 12.8 us, 5.2 TB/s; 16 rows
+// 19.5).  From 17 rows on the tiles are as fast or faster: 32 rows of 8192 x 8192 20.0 us against 29.6 with two groups of
+// 16 rows here, 64 rows 22.1 against 45.8 (20 rows of 2048 x 8192 16.1 against 12.8 is the one loss seen).
 // The 16x16x128 instruction takes row l % 16 and 32 of the panel's columns from lane l; which 32 is the same on
 // both sides, so a lane takes the chunks that make its two loads whole 64-byte runs.  Lane l's results are column
 // l % 16 (a row of A here) and rows 4 (l / 16) .. + 3 (weight rows).
@@ -224,25 +226,21 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(const uint8_t *code
 // ------------------------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
 
-template <int MT, int KS, int MODE, int AF, bool WIDE>
-__global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Args a, int tiles_n)
+template <int KS, int MODE, int AF, bool WIDE>
+__global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Args a)
 {
-    constexpr int R = 16 / KS, NW = MODE == kProduct ? 1 : 2, AHEAD = (MT > 2 ? 2 : 4) / NW;
-    __shared__ float part[kRowWaves][NW][MT * 256];
+    constexpr int R = 16 / KS, NW = MODE == kProduct ? 1 : 2, AHEAD = 4 / NW;
+    __shared__ float part[kRowWaves][NW][256];
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63, c = l & 15, g = l >> 4;
-    const int slice = c / R, r = c % R;
-    const unsigned tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x - tm * (unsigned)tiles_n;
-    const int m0 = (int)tm * 16 * MT, n0 = (int)tn * R;
-    const int wr = min(n0 + r, a.n - 1);
+    const int slice = c / R, r = c % R, n0 = (int)blockIdx.x * R;
+    const int wr = min(n0 + r, a.n - 1), ar = min(r, a.m - 1);
     const uint8_t *wc[2] = {a.w_codes, a.u_codes}, *wsc[2] = {a.w_scales, a.u_scales};
-    v4f acc[NW][MT];
+    v4f acc[NW];
 #pragma unroll
-    for (int j = 0; j < NW; ++j)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[j][t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < NW; ++j) acc[j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
     for (int p0 = w * KS; p0 < a.k1; p0 += AHEAD * kRowWaves * KS) {
-        v4i wv[AHEAD][NW][2], av[AHEAD][MT][2];
-        int ws[AHEAD][NW], as[AHEAD][MT];
+        v4i wv[AHEAD][NW][2], av[AHEAD][2];
+        int ws[AHEAD][NW], as[AHEAD];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             const int p = p0 + u * kRowWaves * KS + slice;
@@ -258,55 +256,42 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Args a, int
                     ws[u][j] = wsc[j][((long long)(p >> 2) * a.n + wr) * 4 + (p & 3)];
                 }
             }
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                av[u][t][0] = av[u][t][1] = (v4i){0, 0, 0, 0};
-                as[u][t] = 0;
-                if (in) {
-                    const int ar = min(m0 + 16 * t + r, a.m - 1);
-                    const v4i *src = (const v4i *)a.a_codes + ((long long)p * a.m + ar) * 8 + g;
-                    av[u][t][0] = src[0];
-                    av[u][t][1] = src[4];
-                    as[u][t] = a.a_scales[((long long)(p >> 2) * a.m + ar) * 4 + (p & 3)];
-                }
+            av[u][0] = av[u][1] = (v4i){0, 0, 0, 0};
+            as[u] = 0;
+            if (in) {
+                const v4i *src = (const v4i *)a.a_codes + ((long long)p * a.m + ar) * 8 + g;
+                av[u][0] = src[0];
+                av[u][1] = src[4];
+                as[u] = a.a_scales[((long long)(p >> 2) * a.m + ar) * 4 + (p & 3)];
             }
         }
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             if constexpr (WIDE) {
-                lowp_v8b x[MT][4];
-#pragma unroll
-                for (int t = 0; t < MT; ++t) fp8_widen<AF>(av[u][t][0], av[u][t][1], as[u][t], x[t]);
+                lowp_v8b x[4];
+                fp8_widen<AF>(av[u][0], av[u][1], as[u], x);
 #pragma unroll
                 for (int j = 0; j < NW; ++j) {
                     lowp_v8b y[4];
                     fp8_widen<0>(wv[u][j][0], wv[u][j][1], ws[u][j], y);
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[q], x[t][q], acc[j][t], 0, 0, 0);
+                    for (int q = 0; q < 4; ++q) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[q], x[q], acc[j], 0, 0, 0);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < NW; ++j)
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-                        acc[j][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(wv[u][j][0], wv[u][j][1]),
-                                                                                     join(av[u][t][0], av[u][t][1]), acc[j][t], 0,
-                                                                                     AF, 0, ws[u][j], 0, as[u][t]);
+                    acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(wv[u][j][0], wv[u][j][1]), join(av[u][0], av[u][1]),
+                                                                              acc[j], 0, AF, 0, ws[u][j], 0, as[u]);
             }
         }
     }
 #pragma unroll
-    for (int j = 0; j < NW; ++j)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) *(v4f *)&part[w][j][t * 256 + c * 16 + 4 * g] = acc[j][t];
+    for (int j = 0; j < NW; ++j) *(v4f *)&part[w][j][c * 16 + 4 * g] = acc[j];
     __syncthreads();
-    for (int t = threadIdx.x; t < MT * 16 * R; t += 64 * kRowWaves) {
-        const int mi = t / R, ni = t % R;
-        const int m = m0 + mi, n = n0 + ni;
-        if ((KS > 1 && mi >= R) || m >= a.m || n >= a.n) continue;
+    const int t = threadIdx.x;
+    if (t < R * R) {
+        const int m = t / R, ni = t % R, n = n0 + ni;
+        if (m >= a.m || n >= a.n) return;
         float f[NW];
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
@@ -314,7 +299,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Args a, int
 #pragma unroll
             for (int i = 0; i < kRowWaves; ++i)
 #pragma unroll
-                for (int k = 0; k < KS; ++k) f[j] += part[i][j][(mi + k * R) * 16 + ni + k * R];
+                for (int k = 0; k < KS; ++k) f[j] += part[i][j][(m + k * R) * 16 + ni + k * R];
         }
         with_act(a.act, [&](auto act) {
             constexpr int ACT = decltype(act)::value;
@@ -334,12 +319,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Args a, int
     }
 }
 
-template <int MT, int KS, int MODE, int AF, bool WIDE>
+template <int KS, int MODE, int AF, bool WIDE>
 hipError_t launch_rows(const Fp8Args &a, hipStream_t s)
 {
-    const int tiles_n = (a.n - 1) / (16 / KS) + 1;
-    const dim3 grid((unsigned)(((a.m - 1) / (16 * MT) + 1) * tiles_n));
-    hipLaunchKernelGGL((fp8_rows_kernel<MT, KS, MODE, AF, WIDE>), grid, dim3(64 * kRowWaves), 0, s, a, tiles_n);
+    hipLaunchKernelGGL((fp8_rows_kernel<KS, MODE, AF, WIDE>), dim3((unsigned)((a.n - 1) / (16 / KS) + 1)), dim3(64 * kRowWaves), 0,
+                       s, a);
     return hipGetLastError();
 }
 
@@ -347,11 +331,9 @@ template <int MODE, int AF, bool WIDE>
 hipError_t rows_form(const Fp8Args &a, hipStream_t s)
 {
     const int cus = cus_or_default();
-    if (a.m > 32) return launch_rows<4, 1, MODE, AF, WIDE>(a, s);
-    if (a.m > 16) return launch_rows<2, 1, MODE, AF, WIDE>(a, s);
-    if (a.m <= 4 && a.n <= 16 * cus && a.k1 >= 4 * kRowWaves) return launch_rows<1, 4, MODE, AF, WIDE>(a, s);
-    if (a.m <= 8 && a.n <= 16 * cus && a.k1 >= 2 * kRowWaves) return launch_rows<1, 2, MODE, AF, WIDE>(a, s);
-    return launch_rows<1, 1, MODE, AF, WIDE>(a, s);
+    if (a.m <= 4 && a.n <= 16 * cus && a.k1 >= 4 * kRowWaves) return launch_rows<4, MODE, AF, WIDE>(a, s);
+    if (a.m <= 8 && a.n <= 16 * cus && a.k1 >= 2 * kRowWaves) return launch_rows<2, MODE, AF, WIDE>(a, s);
+    return launch_rows<1, MODE, AF, WIDE>(a, s);
 }
 
 template <int MODE, int AF>
@@ -408,7 +390,7 @@ hipError_t launch_fp8_dequantize(const uint8_t *codes, const uint8_t *scales, in
     return hipGetLastError();
 }
 
-bool fp8_few_rows(int m, int n) { return m <= 64 && n <= 1 << 24; }
+bool fp8_few_rows(int m, int n) { return m <= 16 && n <= 1 << 24; }
 
 hipError_t launch_fp8(Fp8Args a, Fp8Mode mode, hipStream_t s)
 {
@@ -416,11 +398,13 @@ hipError_t launch_fp8(Fp8Args a, Fp8Mode mode, hipStream_t s)
     if (mode == kProduct) return a.a_format ? rows_of_type<kProduct, 1>(a, s) : rows_of_type<kProduct, 0>(a, s);
     if (mode == kGatedGrad) return rows_of_type<kGatedGrad, 0>(a, s);
     if (!a.codes) return rows_of_type<kGated, 0>(a, s);
-    // a block's 128 columns are eight workgroups': their values in 32 bits first, then the rounding
+    // A block's 128 columns are eight workgroups': their values in 32 bits first, then the rounding in a launch of its own
+    // (4 us).  One launch whose workgroups take 128 columns of both weights reads no faster than 35 GB/s a CU: 1 x 8192 x
+    // 2048 18.2 us against 12.1, 1 x 2048 x 8192 59.6 against 12.1 (1 x 1000 x 500 9.4 against 11.7).
     a.y = a.ws;
     a.type = 0;
     a.ld_y = a.n;
-    const hipError_t e = rows_form<kGated, 0, false>(a, s);
+    const hipError_t e = rows_form<kGated, 0, true>(a, s);
     if (e != hipSuccess) return e;
     return launch_fp8_quantize(a.ws, 0, a.n, a.m, a.n, 0, a.codes, a.scales, s);
 }

@@ -452,11 +452,13 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
     }
 }
 
+// TileX moves the fewest bytes to LDS a product and has a CU to itself; two workgroups of the others fit one.  TileG is
+// the product's step between TileM and TileS, and the gated forms' smallest.
 typedef Tile<256, 256, 4, 2, 2> TileX;
 typedef Tile<128, 128, 2, 2, 2> TileM;
+typedef Tile<64, 128, 2, 2, 3> TileG;
 typedef Tile<64, 64, 2, 2, 4> TileS;   // product
-typedef Tile<64, 128, 2, 2, 3> TileG;  // gated, 64 columns
-typedef Tile<64, 256, 2, 2, 3> TileC;  // gated to codes, 128 columns
+typedef Tile<64, 256, 2, 2, 3> TileC;  // gated to codes: a block of 128 columns
 
 template <typename C, int FORM, int AF>
 hipError_t launch(const Fp8Args &a, hipStream_t s)
@@ -489,6 +491,9 @@ hipError_t product(const Fp8Args &a, hipStream_t s)
     const int cus = cus_or_default();
     if (a.type != 0 && tiles<TileX>(a, 256) >= cus) return launch<TileX, kFormProduct, AF>(a, s);
     if (tiles<TileM>(a, 128) >= cus) return launch<TileM, kFormProduct, AF>(a, s);
+    // small tiles are bound by what they read from L2 (us, TileG / TileS): 1024 x 2048 x 2048 (256 of TileG) 8.9 / 10.0,
+    // to float32 with k 6241 30.8 / 34.2; 300 x 4096 x 4096 (160) 13.8 / 14.8; 512 x 2048 x 2048 (128) 8.6 / 7.4
+    if (8 * tiles<TileG>(a, 128) >= 5 * cus) return launch<TileG, kFormProduct, AF>(a, s);
     return launch<TileS, kFormProduct, AF>(a, s);
 }
 

@@ -9,16 +9,18 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
-from typing import List, Optional
+from typing import List, NamedTuple, Optional
 
 import torch
 
 # Images per pass of ifx_net_forward used by the benchmark (0 = whole batch).
 DEFAULT_SUB_BATCH = 0
 
-from . import (ACT_NONE, ACT_SILU, INPUT_NHWC, BlockParams, ConvDesc, NetGraph, NetParams, block_forward, block_workspace_bytes,
-               conv_desc, conv_fused, conv_out_dims, dequantize_i32, group_norm, group_norm_backward, group_norm_mx4, mx4_matmul,
-               mx4_quantize, net_forward, net_workspace_bytes, pack_act, pack_weights, synth, _alloc)
+from . import (ACT_NONE, ACT_SILU, FP8_E5M2, INPUT_NHWC, BlockParams, ConvDesc, Fp8, NetGraph, NetParams, block_forward,
+               block_workspace_bytes, conv_desc, conv_fused, conv_out_dims, dequantize_i32, fp8_dequantize, fp8_matmul,
+               fp8_quantize, fp8_quantize_t, gated_backward, gated_fp8, group_norm, group_norm_backward, group_norm_mx4, mx4_matmul,
+               mx4_quantize, net_forward, net_workspace_bytes, pack_act, pack_weights, rms_norm_backward, rms_norm_fp8, synth,
+               _alloc)
 
 
 @dataclass
@@ -179,3 +181,68 @@ class NormPointwise4:
     def norm_backward(self, dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, stream=None):
         """(dx, dweight, dbias) of norm()."""
         return group_norm_backward(dy, x, mean, rstd, self.groups, self.norm_weight, self.norm_bias, self.act, stream=stream)
+
+
+class FeedForwardState(NamedTuple):
+    """What GatedFeedForward8.forward keeps for its gradient."""
+    q: Fp8            # the normalised rows in 8 bits
+    h: torch.Tensor   # the sum of input and residual
+    rstd: torch.Tensor
+    hidden: Fp8       # the gated pair's result in 8 bits
+
+
+class FeedForwardGrads(NamedTuple):
+    """Gradients of GatedFeedForward8: of x (and the residual, the same) in its type, of the weights in float32."""
+    x: torch.Tensor
+    gate: torch.Tensor
+    up: torch.Tensor
+    down: torch.Tensor
+    norm_weight: torch.Tensor
+
+
+class GatedFeedForward8:
+    """A gated feed-forward layer in 8 bits on a residual stream, a row per token:
+        h = x + residual,  n = rms_norm(h),  y = h + (act(n G^T) * (n U^T)) D^T
+    with n and the gated pair's result rounded to 8 bits as they are computed.
+
+    w_gate and w_up float [hidden, c], w_down float [c, hidden], rounded once, with `train` their transposes too;
+    norm_weight float32 [c].  forward() serves and trains, backward() gives the gradients of what forward() kept: its
+    products round a gradient to `grad_format` with a power of two per block of 128.  A result of a call with a stream is
+    memory of that stream.
+    """
+
+    def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
+                 act: int = ACT_SILU, eps: float = 1e-5, train: bool = False, grad_format: int = FP8_E5M2):
+        weights = (w_gate, w_up, w_down)
+        self.gate, self.up, self.down = (fp8_quantize(w) for w in weights)
+        self.turned = tuple(fp8_quantize_t(w) for w in weights) if train else None
+        self.norm_weight, self.act, self.eps, self.grad_format = norm_weight, act, eps, grad_format
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None):
+        """(y, what backward() needs): y of x's shape and type, x [..., c]."""
+        q, h, rstd = rms_norm_fp8(x, self.norm_weight, residual, self.eps, stream=stream)
+        hidden = gated_fp8(q, self.gate, self.up, self.act, stream=stream)
+        y = fp8_matmul(hidden, self.down, None, h.view(q.rows, q.k), ACT_NONE, x.dtype, stream=stream)
+        return y.view(x.shape), FeedForwardState(q, h, rstd, hidden)
+
+    def backward(self, dy: torch.Tensor, state: FeedForwardState, stream=None) -> FeedForwardGrads:
+        """The gradients for dy of y's shape and type, of one token or more."""
+        if self.turned is None:
+            raise ValueError("a layer made with train=True expected")
+        q, h, rstd, hidden = state
+        gate_t, up_t, down_t = self.turned
+        fmt, dtype = self.grad_format, h.dtype
+        dy2 = dy.view(q.rows, q.k)
+
+        def weight_grad(grad, values):
+            return fp8_matmul(fp8_quantize_t(grad, fmt, stream=stream), values, dtype=torch.float32, stream=stream)
+        # through the projection back, the gated pair, the two projections, the norm
+        dhidden = fp8_matmul(fp8_quantize(dy2, fmt, stream=stream), down_t, dtype=dtype, stream=stream)
+        dgate, dup = gated_backward(dhidden, q, self.gate, self.up, self.act, stream=stream)
+        dn = fp8_matmul(fp8_quantize(dgate, fmt, stream=stream), gate_t, dtype=dtype, stream=stream)
+        fp8_matmul(fp8_quantize(dup, fmt, stream=stream), up_t, None, dn, ACT_NONE, dtype, out=dn, stream=stream)
+        dx, dnorm = rms_norm_backward(dn.view(h.shape), h, rstd, self.norm_weight, dy.view(h.shape), stream=stream)
+        # the weights': sums over tokens, so every operand is rounded along them
+        n_t = fp8_quantize_t(fp8_dequantize(q, dtype, stream=stream), stream=stream)
+        hidden_t = fp8_quantize_t(fp8_dequantize(hidden, dtype, stream=stream), stream=stream)
+        return FeedForwardGrads(dx, weight_grad(dgate, n_t), weight_grad(dup, n_t), weight_grad(dy2, hidden_t), dnorm)

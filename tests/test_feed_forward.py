@@ -1,0 +1,164 @@
+"""The gated feed-forward layer in 8 bits: rounding, norm, gated projections, products and their gradients together."""
+import numpy as np
+import pytest
+import torch
+
+import convolution_int8_implicit_amd as ifx
+from convolution_int8_implicit_amd import model
+from oracle import lowp
+from test_fp8 import sum_bound
+from test_mx4 import TYPES, excess, f64, note
+
+
+def layer(c, hidden, seed=1, act=ifx.ACT_SILU, **kw):
+    gen = torch.Generator().manual_seed(seed)
+    g, u, d = (torch.randn(n, k, generator=gen) / k ** 0.5 for n, k in ((hidden, c), (hidden, c), (c, hidden)))
+    w = 1 + 0.2 * torch.randn(c, generator=gen)
+    return model.GatedFeedForward8(g.cuda(), u.cuda(), d.cuda(), w.cuda(), act, train=True, **kw), (g, u, d, w)
+
+
+def values(q):
+    return lowp.fp8_values(q.codes.cpu().numpy(), q.scales.cpu().numpy(), q.k, q.format)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,c,hidden,kind", [(1, 256, 640, "bf16"), (7, 100, 333, "f16"), (40, 257, 500, "bf16"),
+                                                  (130, 384, 1000, "f32"), (600, 512, 1290, "bf16")])
+def test_layer(tokens, c, hidden, kind):
+    """Every step from the kernels' own operands within its bound, the whole near the formulas in 64 bits."""
+    note(f"layer {tokens} x {c} x {hidden} {kind}")
+    ff, (g, u, d, w) = layer(c, hidden)
+    gen = torch.Generator().manual_seed(tokens)
+    x, r, dy = (torch.randn(tokens, c, generator=gen).to(TYPES[kind]) for _ in range(3))
+    y, st = ff.forward(x.cuda(), r.cuda())
+    assert y.shape == (tokens, c) and y.dtype == TYPES[kind]
+    assert torch.equal(st.h.cpu(), (x.float() + r.float()).to(TYPES[kind]))
+    # the projection back: the product's bound, then one rounding
+    hv, dv, h = values(st.hidden), values(ff.down), f64(st.h)
+    exact = hv @ dv.T + h
+    size = np.abs(hv) @ np.abs(dv).T + np.abs(h)
+    assert excess(f64(y), exact, sum_bound(hidden, kind) * size, kind) == 0
+    # against the layer without rounding to 8 bits.  Each of two rounded operands of the three products is off by at
+    # most 2^-4 of a value (a uniform error: 2^-4 / sqrt(3) in the mean square), so a result by about sqrt(2) of that,
+    # and the gated pair's by twice: 2^-4 sqrt(2 / 3) (1 + sqrt(2)) < 2^-3 of the projection back, twice that allowed
+    n = lowp.rms_norm(h, f64(w), 1e-5)[0]
+    gate, up = n @ f64(g).T, n @ f64(u).T
+    back = (lowp.act(gate, 2) * up) @ f64(d).T
+    if tokens * c > 1000:
+        assert np.linalg.norm(f64(y) - h - back) <= 2.0 ** -2 * np.linalg.norm(back)
+    # the gradients against the formulas without rounding to 8 bits, e5m2 holding 2^-3 of a value
+    grads = ff.backward(dy.cuda(), st)
+    d64 = f64(dy)
+    dhidden = d64 @ f64(d)
+    dgate, dup = lowp.gated_backward(dhidden, gate, up, 2)
+    dx, dnorm = lowp.rms_norm_backward(dgate @ f64(g) + dup @ f64(u), h, f64(st.rstd), f64(w), d64)
+    exact = (dx, dgate.T @ n, dup.T @ n, d64.T @ (lowp.act(gate, 2) * up), dnorm)
+    for name, got, e in zip(grads._fields, grads, exact):
+        assert got.shape == e.shape, name
+        assert got.dtype == (TYPES[kind] if name == "x" else torch.float32), name
+        if tokens > 1:
+            assert np.linalg.norm(f64(got) - e) <= 0.5 * np.linalg.norm(e), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [3, 90])
+def test_gradients_from_their_own_operands(tokens):
+    """Each gradient from the kernels' own intermediate results: the products', the gated pair's and the norm's bounds."""
+    c, hidden = 200, 300
+    ff, (g, u, d, w) = layer(c, hidden)
+    x, dy = (torch.randn(tokens, c, generator=torch.Generator().manual_seed(i)).cuda() for i in (1, 2))
+    _, st = ff.forward(x)
+    grads = ff.backward(dy, st)
+    fmt = ff.grad_format
+    down_t, gate_t, up_t = (lowp.fp8_values(*lowp.fp8_quantize(f64(t).T), t.shape[0]) for t in (d, g, u))
+
+    def rounded(t, f=fmt):
+        return lowp.fp8_values(*lowp.fp8_quantize(t, f), t.shape[1], f)
+    dhidden = ifx.fp8_matmul(ifx.fp8_quantize(dy, fmt), ff.turned[2], dtype=torch.float32)
+    a = rounded(f64(dy))
+    assert excess(f64(dhidden), a @ down_t.T, sum_bound(c, "f32") * (np.abs(a) @ np.abs(down_t).T), "f32") == 0
+    dgate, dup = ifx.gated_backward(dhidden, st.q, ff.gate, ff.up, ff.act)
+    nv = rounded(values(st.q).T, 0)
+    for got, grad in ((grads.gate, dgate), (grads.up, dup)):
+        a = rounded(f64(grad).T)
+        assert excess(f64(got), a @ nv.T, sum_bound(tokens, "f32") * (np.abs(a) @ np.abs(nv).T), "f32") == 0
+    a, hv = rounded(f64(dy).T), rounded(values(st.hidden).T, 0)
+    assert excess(f64(grads.down), a @ hv.T, sum_bound(tokens, "f32") * (np.abs(a) @ np.abs(hv).T), "f32") == 0
+    a, b = rounded(f64(dgate)), rounded(f64(dup))
+    dn = a @ gate_t.T + b @ up_t.T
+    size = np.abs(a) @ np.abs(gate_t).T + np.abs(b) @ np.abs(up_t).T
+    # the norm's gradient passes an error of dn on by at most rstd (|w| + |xhat| mean |w xhat|)
+    dx, dnorm = lowp.rms_norm_backward(dn, f64(x), f64(st.rstd), f64(w), f64(dy))
+    xhat = np.abs(f64(x) * f64(st.rstd)[:, None])
+    err = 2 * sum_bound(hidden, "f32") * size + 2.0 ** -18 * np.abs(dn)
+    wa = np.abs(f64(w))
+    tol = f64(st.rstd)[:, None] * (wa * err + xhat * (wa * err * xhat).mean(-1, keepdims=True)) + 2.0 ** -18 * (
+        np.abs(f64(dy)) + f64(st.rstd)[:, None] * (np.abs(dn) * wa + xhat * (np.abs(dn) * wa * xhat).mean(-1, keepdims=True)))
+    assert (np.abs(f64(grads.x) - dx) <= tol).all()
+    assert (np.abs(f64(grads.norm_weight) - dnorm) <= (err * xhat).sum(0) + 2.0 ** -16 * (np.abs(dn) * xhat).sum(0)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [1, 200])
+def test_layer_in_a_graph_and_on_a_given_stream(tokens):
+    """Replays on new inputs equal eager calls; a stream that is still busy gives the same results."""
+    c, hidden = 256, 640
+    ff, _ = layer(c, hidden)
+    x, r, dy = (torch.randn(2, tokens, c, device="cuda").to(torch.bfloat16) for _ in range(3))
+
+    def both(stream=None):
+        y, st = ff.forward(x, r, stream)
+        return (y, *ff.backward(dy, st, stream))
+    eager = both()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = both()
+    for i in range(4):
+        for t in outs:
+            t.zero_()
+        if i > 1:
+            x.add_(0.5)
+            eager = both()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, eager))
+    work = torch.zeros(1 << 28, device="cuda")
+    s = torch.cuda.Stream()
+    for given in (s, s.cuda_stream):
+        torch.cuda.synchronize()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(8):
+                work.add_(1.0)
+        outs = both(given)
+        fill = [torch.full((2, tokens, hidden), float("nan"), device="cuda") for _ in range(6)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, eager))
+        del fill
+
+
+@pytest.mark.gpu
+def test_layer_of_no_tokens():
+    ff, _ = layer(64, 130)
+    x = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    y, st = ff.forward(x, x)
+    assert y.shape == (0, 64)
+    with pytest.raises(ifx.IfxError):  # sums over no tokens have no blocks
+        ff.backward(x, st)
+    w = torch.ones(130, 64, device="cuda")
+    with pytest.raises(ValueError, match="train"):
+        model.GatedFeedForward8(w, w, w.t().contiguous()).backward(x, st)
+
+
+@pytest.mark.gpu
+def test_a_padded_batch():
+    """Rows behind the last token, of zeros or of NaN, leave the others' results as they are."""
+    ff, _ = layer(256, 640)
+    x = torch.randn(70, 256, device="cuda")
+    y, _ = ff.forward(x)
+    for fill in (0.0, float("nan")):
+        padded = torch.full((100, 256), fill, device="cuda")
+        padded[:70] = x
+        z, _ = ff.forward(padded)
+        assert torch.equal(z[:70], y) and bool((z[70:].isnan() if fill != 0 else z[70:] == 0).all())

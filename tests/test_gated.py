@@ -54,9 +54,9 @@ def test_refusals_need_no_device():
     assert forward(y=None) == 1 and forward(y=odd) == 4 and forward(ld_y=2) == 2
     assert eight(codes=None) == 1 and eight(scales=None) == 1 and eight(codes=half) == 4
     assert eight(ld_y=0, codes=None) == 1  # its pitch is not looked at
-    # up to 64 rows pass through the workspace
-    assert L.ifx_gated_workspace_bytes(desc(m=64, n=1000)) == 64 * 1000 * 4
-    assert L.ifx_gated_workspace_bytes(desc(m=65, n=1000)) == 0 and L.ifx_gated_workspace_bytes(desc(k=0)) == 0
+    # up to 16 rows pass through the workspace
+    assert L.ifx_gated_workspace_bytes(desc(m=16, n=1000)) == 16 * 1000 * 4
+    assert L.ifx_gated_workspace_bytes(desc(m=17, n=1000)) == 0 and L.ifx_gated_workspace_bytes(desc(k=0)) == 0
     assert eight(m=4, ws_bytes=4 * 3 * 4 - 1) == 5 and eight(m=4, ws=None) == 1 and eight(m=4, ws=half) == 4
     for s in ("dy", "dgate", "dup"):
         assert backward(**{s: None}) == 1 and backward(**{s: odd}) == 4
