@@ -1,5 +1,5 @@
 // 8-bit floating point with one power of two per block of 128: rounding, also of the transpose, the values back,
-// and the products for few rows (fp8_gemm.hip holds the tiled ones).
+// and the products for few rows (fp8_tile.h holds the tiled ones).
 //
 // A tensor of `rows` rows and k columns holds blocks of 128 consecutive columns of a row: one byte a column (e4m3
 // or e5m2) and one power of two per block, 2^(s - 127) with the byte s (255: NaN).  The layout is blocked by 128
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(const uint8_t *code
 // KS > 1, for at most 16 / KS rows of A over few weight rows: the instruction's 16 rows are KS panels of 16 / KS
 // weight rows and of as many rows of A, of whose products the KS blocks on the diagonal count, so a workgroup takes
 // 16 / KS weight rows and KS times as many workgroups share the bytes.
-// WIDE: products in bfloat16 (fp8_gemm.hip says when and why).
+// WIDE: products in bfloat16 (fp8_tile.h says when and why).
 // ------------------------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
 
@@ -394,7 +394,7 @@ bool fp8_few_rows(int m, int n) { return m <= 16 && n <= 1 << 24; }
 
 hipError_t launch_fp8(Fp8Args a, Fp8Mode mode, hipStream_t s)
 {
-    if (!fp8_few_rows(a.m, a.n)) return launch_fp8_tiles(a, mode, s);
+    if (!fp8_few_rows(a.m, a.n)) return mode == kProduct ? launch_fp8_product(a, s) : launch_fp8_gated(a, mode, s);
     if (mode == kProduct) return a.a_format ? rows_of_type<kProduct, 1>(a, s) : rows_of_type<kProduct, 0>(a, s);
     if (mode == kGatedGrad) return rows_of_type<kGatedGrad, 0>(a, s);
     if (!a.codes) return rows_of_type<kGated, 0>(a, s);

@@ -261,7 +261,7 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
                                  long long ld, hipStream_t s);
 hipError_t launch_mx4_matmul(const Mx4Args &a, hipStream_t s);
 hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s);  // its tiled form, mx4_gemm.hip
-// 8-bit rounding, values and products, fp8.hip; the tiled forms, fp8_gemm.hip
+// 8-bit rounding, values and products, fp8.hip; the tiled forms, fp8_gemm.hip and fp8_gated.hip
 hipError_t launch_fp8_quantize(const void *x, int type, long long ld, int rows, int k, int format, uint8_t *codes,
                                uint8_t *scales, hipStream_t s);
 hipError_t launch_fp8_quantize_t(const void *x, int type, long long ld, int rows, int k, int format, uint8_t *codes,
@@ -272,7 +272,8 @@ enum Fp8Mode { kProduct, kGated, kGatedGrad };
 // Whether a launch of these sizes takes the few-rows form (whose 8-bit results pass through Fp8Args::ws).
 bool fp8_few_rows(int m, int n);
 hipError_t launch_fp8(Fp8Args a, Fp8Mode mode, hipStream_t s);
-hipError_t launch_fp8_tiles(Fp8Args a, Fp8Mode mode, hipStream_t s);
+hipError_t launch_fp8_product(Fp8Args a, hipStream_t s);
+hipError_t launch_fp8_gated(Fp8Args a, Fp8Mode mode, hipStream_t s);
 // root mean square norm and its gradient, rms.hip
 size_t rms_workspace_bytes(int rows, int c);
 hipError_t launch_rms_norm(RmsArgs a, hipStream_t s);

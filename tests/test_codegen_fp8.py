@@ -10,7 +10,7 @@ import pytest
 
 from test_codegen import CSRC, HIPCC, ROOT, _kernel_resources, barriers_with_pending_reads
 
-SOURCES = ["fp8.hip", "fp8_gemm.hip", "rms.hip"]
+SOURCES = ["fp8.hip", "fp8_gemm.hip", "fp8_gated.hip", "rms.hip"]
 
 
 @pytest.fixture(scope="module")
@@ -48,8 +48,11 @@ def test_no_barrier_with_lds_reads_in_flight(assembly, src):
 
 
 @pytest.mark.parametrize("src,kernel,per_cu", [
-    ("fp8_gemm.hip", "TileILi256ELi256", 1), ("fp8_gemm.hip", "TileILi128ELi128", 2), ("fp8_gemm.hip", "TileILi64ELi128", 2),
-    ("fp8_gemm.hip", "TileILi64ELi64", 2), ("fp8_gemm.hip", "TileILi64ELi256", 1), ("fp8.hip", "fp8_rows_kernel", 2),
+    ("fp8_gemm.hip", "TileILi256ELi256", 1), ("fp8_gemm.hip", "TileILi128ELi128ELi2ELi2ELi2", 2),
+    ("fp8_gemm.hip", "TileILi128ELi128ELi2ELi2ELi4", 1), ("fp8_gemm.hip", "TileILi64ELi128", 2),
+    ("fp8_gemm.hip", "TileILi64ELi64", 2), ("fp8_gated.hip", "TileILi256ELi256", 1),
+    ("fp8_gated.hip", "TileILi128ELi128ELi2ELi2ELi2", 2), ("fp8_gated.hip", "TileILi64ELi128", 2),
+    ("fp8_gated.hip", "TileILi64ELi256", 1), ("fp8_gated.hip", "TileILi128ELi256", 1), ("fp8.hip", "fp8_rows_kernel", 2),
     ("fp8.hip", "fp8_quantize_t_kernel", 8),
 ])
 def test_workgroups_fit_a_cu(assembly, src, kernel, per_cu):

@@ -339,7 +339,7 @@ SHAPES = [(1, 1, 1), (1, 40, 2048), (1, 33, 4224), (2, 17, 33), (3, 50, 4100), (
           (17, 31, 129), (33, 65, 640), (64, 64, 256), (65, 130, 96), (100, 300, 1000), (130, 257, 385), (257, 129, 512),
           (300, 520, 64),
           # enough tiles for the larger ones, edges inside a tile, one to nine steps of the ring
-          (2050, 2049, 300), (2111, 1930, 1100), (4097, 4100, 130), (4200, 3970, 600)]
+          (1000, 1500, 200), (1900, 1700, 700), (2050, 2049, 300), (2111, 1930, 1100), (4097, 4100, 130), (4200, 3970, 600)]
 
 
 @pytest.mark.gpu
