@@ -819,10 +819,14 @@ def fp8_empty(rows: int, k: int, format: int = FP8_E4M3, device="cuda") -> Fp8:
 def _fp8_check(q: Fp8, name: str) -> int:
     """The rows of q."""
     codes, scales, k, _ = q
-    k1, k4 = (k + 127) // 128, (k + 511) // 512
-    rows = codes.shape[1] if codes.dim() == 3 else -1
-    if (codes.shape != (k1, rows, 128) or scales.shape != (k4, rows, 4) or codes.dtype != torch.uint8
-            or scales.dtype != torch.uint8 or not codes.is_contiguous() or not scales.is_contiguous()):
+    k1, k4 = (k + 127) >> 7, (k + 511) >> 9
+    try:
+        panels, rows, width = codes.shape
+        words, same, four = scales.shape
+    except ValueError:
+        panels = rows = width = words = same = four = -1
+    if (panels != k1 or width != 128 or words != k4 or same != rows or four != 4 or codes.dtype is not torch.uint8
+            or scales.dtype is not torch.uint8 or not codes.is_contiguous() or not scales.is_contiguous()):
         raise ValueError(f"{name}: contiguous uint8 codes [{k1}, rows, 128] and scales [{k4}, rows, 4] expected for k = {k}")
     return rows
 
@@ -836,8 +840,8 @@ def _fp8_out(out: Optional[Fp8], rows: int, k: int, format: int, like: torch.Ten
     return out
 
 
-def _e4m3(q: Fp8, name: str) -> None:
-    if q.format != FP8_E4M3:
+def _e4m3(format: int, name: str) -> None:
+    if format != FP8_E4M3:
         raise ValueError(f"{name}: format FP8_E4M3 expected")
 
 
@@ -900,7 +904,7 @@ def fp8_matmul(a: Fp8, w: Fp8, bias: Optional[torch.Tensor] = None, residual: Op
     m, n = _fp8_check(a, "a"), _fp8_check(w, "w")
     if a.k != w.k:
         raise ValueError(f"a of {a.k} columns, w of {w.k}")
-    _e4m3(w, "w")
+    _e4m3(w.format, "w")
     _fits(m, n, a.k, act, a.format)
     _param(bias, n, "bias")
     ld_y = ld_res = n
@@ -925,8 +929,7 @@ def _gated_desc(x: Fp8, w_gate: Fp8, w_up: Fp8, act: int, dtype: torch.dtype) ->
     m, n = _fp8_check(x, "x"), _fp8_check(w_gate, "w_gate")
     if _fp8_check(w_up, "w_up") != n or not x.k == w_gate.k == w_up.k:
         raise ValueError(f"x of {x.k} columns, w_gate of {n} x {w_gate.k}, w_up of {w_up.rows} x {w_up.k}")
-    for q, name in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
-        _e4m3(q, name)
+    _e4m3(x.format or w_gate.format or w_up.format, "x, w_gate and w_up")
     _fits(m, n, x.k, act)
     return GatedDesc(m, n, x.k, _type(dtype), act, n, n, n)
 

@@ -347,29 +347,47 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
         };
         typedef unsigned QuadWords __attribute__((ext_vector_type(sizeof(E)), aligned(sizeof(E))));
         // A tile that lies whole in the result: addresses are a uniform base and the lane's offset, nothing is
-        // predicated.  RES: an operand is read.
+        // predicated.  RES: an operand is read.  (Eight columns a lane, 16-byte accesses, and all operands requested at
+        // once measured the same.)
         auto whole = [&](auto act, auto res_tag, auto past) __attribute__((always_inline)) {
             constexpr bool RES = decltype(res_tag)::value;
             const unsigned off = (unsigned)((lr * (int)a.ld_y + lc) * (int)sizeof(E));
             const unsigned off2 = FORM == kFormGrad ? (unsigned)((lr * (int)a.ld_y2 + lc) * (int)sizeof(E)) : 0u;
             const unsigned off_r = RES ? (unsigned)((lr * (int)a.ld_res + lc) * (int)sizeof(E)) : 0u;
-            const auto put = [&](void *y, long long ld, int row, unsigned o, Quad<E> v) __attribute__((always_inline)) {
-                char *const base = (char *)y + (row * ld + c0) * (long long)sizeof(E);
+            // the passes' uniform bases, on by RPP rows each time
+            const auto base_of = [&](const void *p, long long ld) __attribute__((always_inline)) {
+                return (char *)p + (r0 * ld + c0) * (long long)sizeof(E);
+            };
+            const long long step_y = RPP * a.ld_y * (long long)sizeof(E), step_y2 = RPP * a.ld_y2 * (long long)sizeof(E);
+            const long long step_r = RPP * a.ld_res * (long long)sizeof(E);
+            char *y = base_of(a.y, a.ld_y), *y2 = FORM == kFormGrad ? base_of(a.y2, a.ld_y2) : nullptr;
+            const char *r_at = RES ? base_of(a.res, a.ld_res) : nullptr;
+            const auto put = [&](char *&base, long long step, unsigned o, const float (&f)[4]) __attribute__((always_inline)) {
+                QuadWords v;
+                if constexpr (sizeof(E) == 4) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(f[e]);
+                } else {
+                    v[0] = pack2<E>(f[0], f[1]);
+                    v[1] = pack2<E>(f[2], f[3]);
+                }
                 if constexpr (decltype(past)::value) {
-                    __builtin_nontemporal_store(__builtin_bit_cast(QuadWords, v), (QuadWords *)(base + o));
+                    __builtin_nontemporal_store(v, (QuadWords *)(base + o));
                     keep_apart();
                 } else {
-                    *(Quad<E> *)(base + o) = v;
+                    *(QuadWords *)(base + o) = v;
                 }
+                base += step;
             };
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
-                const int row = r0 + i * 32;
                 Quad<E> res[P];
                 if constexpr (RES) {  // requested before the rows are staged
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        res[p] = *(const Quad<E> *)((const char *)a.res + ((row + p * RPP) * a.ld_res + c0) * (long long)sizeof(E) + off_r);
+                    for (int p = 0; p < P; ++p) {
+                        res[p] = *(const Quad<E> *)(r_at + off_r);
+                        r_at += step_r;
+                    }
                 }
                 stage(act, i);
 #pragma unroll
@@ -377,15 +395,15 @@ __global__ __launch_bounds__(C::T, waves_per_simd(C::T, C::PER_CU > 2 ? 2 : C::P
                     const v4f f = *(const v4f *)(src + p * RPP * C::ROW);
                     v4f u = {};
                     if constexpr (FORM == kFormGrad) u = *(const v4f *)(src + p * RPP * C::ROW + TO * 4);
-                    Quad<E> q, q2;
+                    float q[4], q2[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float r = RES ? (float)res[p].v[e] : 0.0f, v = FORM == kFormProduct ? f[e] + bias[e] : f[e];
-                        q.v[e] = (E)(RES || FORM != kFormProduct ? first(act, v, u[e], r) : act_of<decltype(act)::value>(v));
-                        if constexpr (FORM == kFormGrad) q2.v[e] = (E)second(act, v, r);
+                        q[e] = RES || FORM != kFormProduct ? first(act, v, u[e], r) : act_of<decltype(act)::value>(v);
+                        if constexpr (FORM == kFormGrad) q2[e] = second(act, v, r);
                     }
-                    put(a.y, a.ld_y, row + p * RPP, off, q);
-                    if constexpr (FORM == kFormGrad) put(a.y2, a.ld_y2, row + p * RPP, off2, q2);
+                    put(y, step_y, off, q);
+                    if constexpr (FORM == kFormGrad) put(y2, step_y2, off2, q2);
                 }
                 wave_lds_sync();
             }

@@ -214,8 +214,8 @@ __device__ __forceinline__ float act_slope(float z)
 {
     if (ACT == 1) return z > 0.0f ? 1.0f : 0.0f;
     if (ACT == 2) {
-        const float s = sigmoid(z);
-        return s * fmaf(z, 1.0f - s, 1.0f);
+        const float s = sigmoid(z), a = z * s;  // (the activation itself, which a caller has too)
+        return fmaf(a, 1.0f - s, s);
     }
     return 1.0f;
 }
