@@ -1758,7 +1758,7 @@ ifx_status ifx_rms_norm_fp8(const ifx_rms_desc *d, const void *x, const void *re
 
 size_t ifx_rms_norm_workspace_bytes(const ifx_rms_desc *d)
 {
-    return check_rms(d) == IFX_OK ? ifx::rms_workspace_bytes(d->rows, d->c) : 0;
+    return check_rms(d) == IFX_OK ? ifx::rms_workspace_bytes(d->rows, d->c, d->type) : 0;
 }
 
 ifx_status ifx_rms_norm_backward(const ifx_rms_desc *d, const void *dy, const void *h, const float *rstd,
@@ -1780,7 +1780,7 @@ ifx_status ifx_rms_norm_backward(const ifx_rms_desc *d, const void *dy, const vo
         if (st == IFX_OK) st = check_operand(d, dh, d->ld_dh);
         if (st != IFX_OK) return st;
         if (!aligned_to(weight, 4) || !aligned_to(rstd, 4) || !aligned16(ws)) return IFX_E_ALIGN;
-        const size_t need = dweight ? ifx::rms_workspace_bytes(d->rows, d->c) : 0;
+        const size_t need = dweight ? ifx::rms_workspace_bytes(d->rows, d->c, d->type) : 0;
         if (need > ws_bytes) return IFX_E_WORKSPACE;
         if (need > 0 && !ws) return IFX_E_NULL;
         a.x = h;

@@ -275,7 +275,7 @@ hipError_t launch_fp8(Fp8Args a, Fp8Mode mode, hipStream_t s);
 hipError_t launch_fp8_product(Fp8Args a, hipStream_t s);
 hipError_t launch_fp8_gated(Fp8Args a, Fp8Mode mode, hipStream_t s);
 // root mean square norm and its gradient, rms.hip
-size_t rms_workspace_bytes(int rows, int c);
+size_t rms_workspace_bytes(int rows, int c, int type);
 hipError_t launch_rms_norm(RmsArgs a, hipStream_t s);
 hipError_t launch_rms_norm_grad(RmsArgs a, float *dweight, hipStream_t s);
 // group norm with an activation and its gradient, norm.hip

@@ -357,32 +357,45 @@ hipError_t launch_rows(const RmsArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <int TPR, int NV, bool WHOLE = true>
+// TYPES: the float32 (1) and the 16-bit (2) instances that the plan below may take.
+template <int TPR, int NV, bool WHOLE = true, int TYPES = 3>
 hipError_t launch_grad(const RmsArgs &a, hipStream_t s)
 {
     // float32 rows past 8192 columns and any past 16384 leave no registers for a second row
-    auto *f = a.type == 0 ? rms_grad_kernel<0, TPR, NV, (TPR * NV < 2048), WHOLE>
-              : a.type == 1 ? rms_grad_kernel<1, TPR, NV, (TPR * NV < 3072), WHOLE>
-                            : rms_grad_kernel<2, TPR, NV, (TPR * NV < 3072), WHOLE>;
+    void (*f)(RmsArgs) = nullptr;
+    if constexpr (TYPES & 1)
+        if (a.type == 0) f = rms_grad_kernel<0, TPR, NV, (TPR * NV < 2048), WHOLE>;
+    if constexpr (TYPES & 2) {
+        if (a.type == 1) f = rms_grad_kernel<1, TPR, NV, (TPR * NV < 3072), WHOLE>;
+        if (a.type == 2) f = rms_grad_kernel<2, TPR, NV, (TPR * NV < 3072), WHOLE>;
+    }
     hipLaunchKernelGGL(f, dim3((unsigned)a.chunks), dim3(threads_of(TPR)), 0, s, a);
     return hipGetLastError();
 }
 
-// Threads that share a row in the gradient, and the rows of a workgroup.
-int grad_tpr(int c) { return c <= 128 ? 16 : c <= 1024 ? 64 : c <= 8192 ? 256 : 1024; }
+// Threads that share a row in the gradient.  From 4097 to 8192 columns (us, 256 threads / 512 / 1024): 8192 x 8192 bf16
+// 106 / 88 / 97, 3000 x 8000 float32 79 / 69 / 62.
+int grad_tpr(int c, int type)
+{
+    return c <= 128 ? 16 : c <= 1024 ? 64 : c <= 4096 ? 256 : c <= 8192 && type != 0 ? 512 : 1024;
+}
 
 // Workgroups of the gradient: two a CU of the 256 that an MI355X has (no device is asked: this sizes the caller's
-// workspace too), at most one a row (or few rows).
-int grad_chunks(int rows, int c)
+// workspace too), one where it fills the CU (4000 x 15000 bf16 98 / 91 us, two / one a CU) or half of it with few rows to
+// take (700 x 8192 18.1 / 16.5; but 1517 x 510 float16 12.9 / 13.9), at most one a row (or few rows).
+int grad_chunks(int rows, int c, int type)
 {
-    const int rpb = threads_of(grad_tpr(c)) / grad_tpr(c);
-    const int most = (rows - 1) / rpb + 1;
-    return most < 512 ? most : 512;
+    const int tpr = grad_tpr(c, type), rpb = threads_of(tpr) / tpr;
+    const int groups = (rows - 1) / rpb + 1, most = tpr == 1024 || (tpr == 512 && groups < 2048) ? 256 : 512;
+    return groups < most ? groups : most;
 }
 
 }  // namespace
 
-size_t rms_workspace_bytes(int rows, int c) { return rows > 0 ? (size_t)grad_chunks(rows, c) * (size_t)c * 4 : 0; }
+size_t rms_workspace_bytes(int rows, int c, int type)
+{
+    return rows > 0 ? (size_t)grad_chunks(rows, c, type) * (size_t)c * 4 : 0;
+}
 
 hipError_t launch_rms_norm(RmsArgs a, hipStream_t s)
 {
@@ -404,19 +417,19 @@ hipError_t launch_rms_norm(RmsArgs a, hipStream_t s)
 hipError_t launch_rms_norm_grad(RmsArgs a, float *dweight, hipStream_t s)
 {
     if (a.rows > 0) {
-        a.chunks = grad_chunks(a.rows, a.c);
+        a.chunks = grad_chunks(a.rows, a.c, a.type);
         a.past = stored_past(a.y, a.rows, a.ld_y, a.type == 0 ? 4 : 2);
         if (!dweight)
             a.part = nullptr;
         else if (a.chunks == 1)
             a.part = dweight;  // the only row of partial sums
         const hipError_t e = a.c < 8        ? launch_grad<16, 1, false>(a, s)
-                             : a.c <= 128  ? launch_grad<16, 1>(a, s)
-                             : a.c <= 512  ? launch_grad<64, 1>(a, s)
-                             : a.c <= 1024 ? launch_grad<64, 2>(a, s)
-                             : a.c <= 2048 ? launch_grad<256, 1>(a, s)
-                             : a.c <= 4096 ? launch_grad<256, 2>(a, s)
-                             : a.c <= 8192 ? launch_grad<256, 4>(a, s)
+                             : a.c <= 128   ? launch_grad<16, 1>(a, s)
+                             : a.c <= 512   ? launch_grad<64, 1>(a, s)
+                             : a.c <= 1024  ? launch_grad<64, 2>(a, s)
+                             : a.c <= 2048  ? launch_grad<256, 1>(a, s)
+                             : a.c <= 4096  ? launch_grad<256, 2>(a, s)
+                             : a.c <= 8192  ? (a.type == 0 ? launch_grad<1024, 1, true, 1>(a, s) : launch_grad<512, 2, true, 2>(a, s))
                              : a.c <= 16384 ? launch_grad<1024, 2>(a, s)
                                             : launch_grad<1024, 3>(a, s);
         if (e != hipSuccess || !dweight || a.chunks == 1) return e;

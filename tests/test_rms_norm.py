@@ -5,8 +5,8 @@ Bounds.  A row's sum of squares is a chain of at most 24 fused additions a threa
 wave and 16 across waves, each off by at most 2^-24 of the sum, so rstd is off by at most 23 2^-24 of itself for the sum and
 4 roundings for the rest: 2^-19.  y = h rstd weight adds two roundings: 2^-18 of itself in all, then one rounding to the
 type.  The gradient's mean is a chain of as many additions of terms of three roundings: at most 50 2^-24 mean |d xhat|.
-dweight's column is a chain over a workgroup's rows (at most ceil(rows / 512) of them and 16 subgroups), 16 joins a lane and
-32 across: n = rows / 512 + 66 additions of terms of two roundings, off by at most (n + 2) 2^-24 of the terms' magnitudes.
+dweight's column is a chain over a workgroup's rows (at most ceil(rows / 256) of them and 16 subgroups), 16 joins a lane and
+32 across: n = rows / 256 + 66 additions of terms of two roundings, off by at most (n + 2) 2^-24 of the terms' magnitudes.
 """
 import ctypes
 
@@ -144,7 +144,7 @@ def check_grad(dx, dw, dy, h, rstd, w, dh, kind):
     if dh is not None:
         tol = tol + (np.abs(f64(dh)) + np.abs(ex)) * 2.0 ** -23
     assert excess(f64(dx), ex, tol, kind) == 0
-    n = h64.shape[0] // 512 + 66
+    n = h64.shape[0] // 256 + 66
     assert (np.abs(f64(dw) - ew) <= (n + 2) * 2.0 ** -24 * np.abs(d64 * xhat).sum(0)).all()
 
 
@@ -174,7 +174,7 @@ def test_norm_and_gradient(rows, c):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows,c,kind", [(5000, 510, "f16"), (40000, 100, "bf16"), (4111, 1000, "f32"), (3001, 4096, "bf16"),
-                                         (1100, 8192, "f32"), (1050, 9000, "bf16"), (1030, 20000, "bf16")])
+                                         (1100, 8192, "f32"), (2100, 6001, "f16"), (1050, 9000, "bf16"), (1030, 20000, "bf16")])
 def test_many_rows(rows, c, kind):
     """Workgroups that take several rows in turn, results past the caches' size among them."""
     note(f"rms norm {rows} x {c} {kind}")
