@@ -242,7 +242,7 @@ class GatedFeedForward8:
         dn = fp8_matmul(fp8_quantize(dgate, fmt, stream=stream), gate_t, dtype=dtype, stream=stream)
         fp8_matmul(fp8_quantize(dup, fmt, stream=stream), up_t, None, dn, ACT_NONE, dtype, out=dn, stream=stream)
         dx, dnorm = rms_norm_backward(dn.view(h.shape), h, rstd, self.norm_weight, dy.view(h.shape), stream=stream)
-        # the weights': sums over tokens, so every operand is rounded along them
-        n_t = fp8_quantize_t(fp8_dequantize(q, dtype, stream=stream), stream=stream)
-        hidden_t = fp8_quantize_t(fp8_dequantize(hidden, dtype, stream=stream), stream=stream)
+        # the weights': sums over tokens, so every operand is rounded along them; bfloat16 holds an 8-bit value whole, where
+        # float16 overflows
+        n_t, hidden_t = (fp8_quantize_t(fp8_dequantize(t, torch.bfloat16, stream=stream), stream=stream) for t in (q, hidden))
         return FeedForwardGrads(dx, weight_grad(dgate, n_t), weight_grad(dup, n_t), weight_grad(dy2, hidden_t), dnorm)

@@ -162,3 +162,20 @@ def test_a_padded_batch():
         padded[:70] = x
         z, _ = ff.forward(padded)
         assert torch.equal(z[:70], y) and bool((z[70:].isnan() if fill != 0 else z[70:] == 0).all())
+
+
+@pytest.mark.gpu
+def test_hidden_values_past_float16():
+    """The gated pair's result is never of the layer's type: values that float16 does not hold reach the projection back
+    and its weight's gradient.  All values are powers of two and all sums exact."""
+    note("layer float16, hidden values of 2^18")
+    c, hidden, tokens = 128, 64, 30
+    full = lambda *shape, v: torch.full(shape, v, dtype=torch.float16, device="cuda")
+    ff = model.GatedFeedForward8(full(hidden, c, v=4.0), full(hidden, c, v=4.0), full(c, hidden, v=2.0 ** -12), None, eps=0.0,
+                                 train=True)
+    y, st = ff.forward(full(tokens, c, v=1.0))
+    assert (values(st.hidden) == 2.0 ** 18).all()
+    assert torch.equal(y, full(tokens, c, v=1.0 + 64 * 64))  # 4097 rounds to 4096 in float16
+    grads = ff.backward(full(tokens, c, v=2.0 ** -10), st)
+    assert torch.equal(grads.down, torch.full((c, hidden), tokens * 2.0 ** 8, device="cuda"))
+    assert all(bool(torch.isfinite(g).all()) for g in grads)
