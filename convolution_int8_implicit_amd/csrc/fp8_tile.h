@@ -1,6 +1,7 @@
 // The kernel of the tiled products of 8-bit tensors for more than a few rows (fp8.hip holds the layout, the rounding and
-// the products for few rows; fp8_gemm.hip and fp8_gated.hip choose the tiles): y = act(A W^T + bias + residual), the gated pair act(A G^T) (A U^T) to the type or to 8-bit
-// codes, and the pair's gradient dG = dy (A U^T) act'(A G^T), dU = dy act(A G^T).
+// the products for few rows; fp8_gemm.hip and fp8_gated.hip choose the tiles): y = act(A W^T + bias + residual), the gated
+// pair act(A G^T) (A U^T) to the type or to 8-bit codes, and the pair's gradient dG = dy (A U^T) act'(A G^T), dU = dy
+// act(A G^T).
 //
 // A workgroup computes a BM x BN tile in steps of one 128-column panel; in the gated forms the BN weight rows are BN / 2
 // of each weight, so a lane holds both projections of its outputs and they meet in registers.  A step's operands, BM +
@@ -22,6 +23,10 @@
 //
 // A step's second half is read while its first half multiplies, the next step's first half while the second multiplies,
 // across the one barrier of the step; stage s + ST is requested once stage s is read.
+//
+// What bounds it: 8192 x 8192 x 8192 in 256 x 256 tiles takes 405 to 415 us, 2.7 POP/s, at a clock that power holds near
+// 1.6 GHz.  A workgroup takes 4.5 k cycles until its first panel, 142 k for 64 steps (92 % of them the matrix units' own)
+// and 10 k to store the tile; at k = 2048 the first and the last are a third of its time (2.3 POP/s).
 #pragma once
 
 #include <type_traits>

@@ -606,7 +606,8 @@ enum { IFX_FP8_E4M3 = 0, IFX_FP8_E5M2 = 1 };
  * `type` does not hold them.
  *   x, y    DEVICE, of `type`, aligned to the element
  *   codes   DEVICE, ifx_fp8_code_bytes, 16-byte aligned
- *   scales  DEVICE, ifx_fp8_scale_bytes, 4-byte aligned
+ *   scales  DEVICE, ifx_fp8_scale_bytes, 4-byte aligned; codes and scales that
+ *           a call writes, here and below, may not overlap another operand
  *   rows    >= 0 (0: nothing to do, pointers are not looked at); k >= 1; at
  *           most 2^32 / 256 tiles of 16 rows and 512 columns (transposed also:
  *           of 32 rows and 128 columns, and rows <= 2^31 - 65)
