@@ -367,8 +367,8 @@ hipError_t launch_grad(const RmsArgs &a, hipStream_t s)
     if constexpr (TYPES & 1)
         if (a.type == 0) f = rms_grad_kernel<0, TPR, NV, (TPR * NV < 2048), WHOLE>;
     if constexpr (TYPES & 2) {
-        if (a.type == 1) f = rms_grad_kernel<1, TPR, NV, (TPR * NV < 3072), WHOLE>;
-        if (a.type == 2) f = rms_grad_kernel<2, TPR, NV, (TPR * NV < 3072), WHOLE>;
+        if (a.type == 1) f = rms_grad_kernel<1, TPR, NV, (TPR * NV <= 2048), WHOLE>;
+        if (a.type == 2) f = rms_grad_kernel<2, TPR, NV, (TPR * NV <= 2048), WHOLE>;
     }
     hipLaunchKernelGGL(f, dim3((unsigned)a.chunks), dim3(threads_of(TPR)), 0, s, a);
     return hipGetLastError();
