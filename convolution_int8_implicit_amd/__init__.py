@@ -991,29 +991,46 @@ def _rms_desc(x: torch.Tensor, eps: float) -> RmsDesc:
     return RmsDesc(rows, c, _type(x.dtype), eps, ld, c, c, c, c, c)
 
 
-def _rms_forward(x, weight, residual, eps, sum_out, stream):
-    """The descriptor, the sum (x itself without a residual, unless sum_out is given) and whether it is written."""
+def _shares(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors of one shape and type, rows at a pitch each (_pitch), have an element in common."""
+    rows, c, ld = _pitch(a)
+    ld_b = _pitch(b)[2]
+    d = (b.data_ptr() - a.data_ptr()) // a.element_size()
+    if rows == 0 or d >= (rows - 1) * ld + c or -d >= (rows - 1) * ld_b + c:
+        return False
+    # side by side in the rows of a wider tensor, or not
+    return ld != ld_b or d % ld < c or ld - d % ld < c
+
+
+def _rms_forward(x, weight, residual, eps, sum_out, stream, out=None):
+    """The descriptor, the sum (x itself without a residual, unless sum_out is given or `out` takes x's place) and
+    whether it is written."""
     d = _rms_desc(x, eps)
     _param(weight, d.c, "weight")
     if residual is not None:
         d.ld_res = _like(residual, x, "residual")
+    if out is not None:
+        d.ld_y = _like(out, x, "out")
     if sum_out is not None:
         d.ld_h = _like(sum_out, x, "sum_out")
+        if out is not None and _shares(out, sum_out):
+            raise ValueError("out and sum_out share memory")
         return d, sum_out, True
-    return (d, x, False) if residual is None else (d, _alloc(x, stream, x.dtype, *x.shape), True)
+    if residual is None and (out is None or not _shares(out, x)):
+        return d, x, False
+    return d, _alloc(x, stream, x.dtype, *x.shape), True
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
              eps: float = 1e-5, out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None, stream=None):
     """Root mean square norm of h = x + residual over the last axis (ifx_rms_norm) -> (y, h, rstd): y and h of x's
-    shape and type, rstd float32 [rows].  Without a residual h is x itself.  sum_out may be x or the residual, out may
-    be either too, but not sum_out.  Records nothing for autograd: rms_norm_backward gives the gradient."""
+    shape and type, rstd float32 [rows].  Without a residual h is x itself, unless out takes its place.  sum_out may be x
+    or the residual, out may be either too, but not sum_out.  Records nothing for autograd: rms_norm_backward gives the
+    gradient."""
     index = _on_device(x, weight, residual, out, sum_out)
-    d, h, written = _rms_forward(x, weight, residual, eps, sum_out, stream)
+    d, h, written = _rms_forward(x, weight, residual, eps, sum_out, stream, out)
     if out is None:
         out = _alloc(x, stream, x.dtype, *x.shape)
-    else:
-        d.ld_y = _like(out, x, "out")
     rstd = _alloc(x, stream, torch.float32, d.rows)
     _check(lib().ifx_rms_norm(d, x.data_ptr(), _addr(residual), _addr(weight), h.data_ptr() if written else None,
                               out.data_ptr(), rstd.data_ptr(), _raw_stream(stream, index)), "ifx_rms_norm")

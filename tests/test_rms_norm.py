@@ -112,6 +112,51 @@ def test_binding_refusals_need_no_device(monkeypatch):
         ifx.rms_norm_backward(x, x, t(4), out=t(4, 32, dtype=torch.bfloat16))
 
 
+class Recorded:
+    """Stands in for the library: keeps the arguments of the last call."""
+
+    def ifx_rms_norm(self, d, x, res, weight, h, y, rstd, stream):
+        self.h, self.y, self.ld_h, self.ld_y = h, y, d.ld_h, d.ld_y
+        return 0
+
+
+def test_shared_memory_needs_no_device(monkeypatch):
+    """Without a residual the sum is x itself, but not where out takes x's place: then it is memory of its own.  out and
+    sum_out may not share memory."""
+    monkeypatch.setattr(ifx, "_on_device", lambda *ts: 0)
+    monkeypatch.setattr(ifx, "_raw_stream", lambda stream, index: 0)
+    rec = Recorded()
+    monkeypatch.setattr(ifx, "lib", lambda: rec)
+    wide = torch.zeros(4, 80)
+    for x in (torch.zeros(4, 32), wide[:, 3:35], wide.view(2, 2, 80)[..., 1:33]):
+        y, h, _ = ifx.rms_norm(x)
+        assert h is x and rec.h is None
+        y, h, _ = ifx.rms_norm(x, out=torch.zeros_like(x))
+        assert h is x and rec.h is None
+        y, h, _ = ifx.rms_norm(x, out=x)
+        assert y is x and rec.y == x.data_ptr() and rec.ld_y == ifx._pitch(x)[2]
+        assert h.shape == x.shape and rec.h == h.data_ptr() != x.data_ptr() and rec.ld_h == 32
+        y, h, _ = ifx.rms_norm(x, residual=torch.zeros_like(x), out=x)
+        assert y is x and h is not x and rec.h == h.data_ptr()
+        for kw in (dict(out=x, sum_out=x), dict(out=x, sum_out=x, residual=torch.zeros_like(x))):
+            with pytest.raises(ValueError, match="share"):
+                ifx.rms_norm(x, **kw)
+        y, h, _ = ifx.rms_norm(x, out=torch.zeros_like(x), sum_out=x)
+        assert h is x and rec.h == x.data_ptr()
+    # side by side in wider rows they share nothing, one element further they do
+    ifx.rms_norm(torch.zeros(4, 32), out=wide[:, 3:35], sum_out=wide[:, 35:67])
+    ifx.rms_norm(torch.zeros(4, 32), out=wide[:, 48:], sum_out=wide[:, 16:48])
+    for a, b in ((3, 34), (34, 3), (48, 17)):
+        with pytest.raises(ValueError, match="share"):
+            ifx.rms_norm(torch.zeros(4, 32), out=wide[:, a:a + 32], sum_out=wide[:, b:b + 32])
+    flat = torch.zeros(256)
+    ifx.rms_norm(torch.zeros(4, 32), out=flat[:128].view(4, 32), sum_out=flat[128:].view(4, 32))
+    with pytest.raises(ValueError, match="share"):
+        ifx.rms_norm(torch.zeros(4, 32), out=flat[:128].view(4, 32), sum_out=flat[127:255].view(4, 32))
+    none = torch.zeros(0, 32)
+    ifx.rms_norm(none, out=none, sum_out=none)
+
+
 # ------------------------------------------------------------------------------------------ GPU
 
 # every row width at the edges of the kernels' ranges, many rows and few, rows inside a workgroup's group
@@ -222,6 +267,25 @@ def test_pitches_in_place_and_stream(rows, c, off):
             dx1, dw1 = ifx.rms_norm_backward(dy1, h1, rstd, w, dh1, out=out, stream=s)
             s.synchronize()
             assert dx1 is out and torch.equal(out, dx) and torch.equal(dw1, dw) and clean(wide)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,c", [(3, 50), (520, 4096), (5, 20000)])
+def test_in_place_without_a_residual(rows, c):
+    """y over x: the sum that comes back is still x, and its gradient that of plain tensors."""
+    for kind in ("bf16", "f32"):
+        note(f"rms norm over its input, {rows} x {c} {kind}")
+        x, _, dy, dh, w = (t.cuda() for t in rms_case(rows, c, kind, 6))
+        y, _, rstd = ifx.rms_norm(x, w)
+        dx, dw = ifx.rms_norm_backward(dy, x, rstd, w, dh)
+        wide = torch.full((rows, c + 9), 3.0, dtype=TYPES[kind], device="cuda")
+        x1 = wide[:, 4:4 + c]
+        x1.copy_(x)
+        y1, h1, rstd1 = ifx.rms_norm(x1, w, out=x1)
+        assert y1 is x1 and torch.equal(x1, y) and torch.equal(h1, x) and torch.equal(rstd1, rstd)
+        assert (wide[:, :4] == 3).all() and (wide[:, 4 + c:] == 3).all()
+        dx1, dw1 = ifx.rms_norm_backward(dy, h1, rstd1, w, dh)
+        assert torch.equal(dx1, dx) and torch.equal(dw1, dw)
 
 
 @pytest.mark.gpu
