@@ -208,11 +208,11 @@ __device__ __forceinline__ float act_of(float z)
     return z;
 }
 
-// The derivative of an activation, for a ReLU 0 where z <= 0.
+// The derivative of an activation, for a ReLU 0 where z <= 0.  A NaN stays a NaN.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z)
 {
-    if (ACT == 1) return z > 0.0f ? 1.0f : 0.0f;
+    if (ACT == 1) return z <= 0.0f ? 0.0f : z > 0.0f ? 1.0f : z;
     if (ACT == 2) {
         const float s = sigmoid(z), a = z * s;  // (the activation itself, which a caller has too)
         return fmaf(a, 1.0f - s, s);

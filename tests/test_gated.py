@@ -280,6 +280,30 @@ def test_nan_blocks(m):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+@pytest.mark.parametrize("m", [2, 40, 300])
+def test_nan_blocks_of_the_gate(m, act):
+    """A NaN at the gate reaches the gate's gradient whatever the activation, also where the other projection is finite;
+    one at the other projection leaves the other's gradient as it is."""
+    n, k = 300, 200
+    note(f"NaN at the gate, {m} rows, {act}")
+    q, _ = gated_case(m, n, k, 7)
+    q[0][1][0, 1, 1] = 255
+    q[1][1][0, 5, 0] = 255
+    q[1][0][1, 290, 4] = 0xff
+    q[2][0][0, 200, 3] = 0x7f
+    X, G, U = (tensor_of(t, k) for t in q)
+    for kind in ("bf16", "f32"):
+        dy = torch.ones(m, n, dtype=TYPES[kind], device="cuda")
+        dgate, dup = ifx.gated_backward(dy, X, G, U, ACTS[act])
+        at_gate, at_up = (torch.zeros(m, n, dtype=torch.bool, device="cuda") for _ in range(2))
+        at_gate[1] = at_up[1] = at_gate[:, 5] = at_gate[:, 290] = at_up[:, 200] = True
+        # dgate = dy up act'(gate), dup = dy act(gate); without an activation act' is 1 whatever the gate
+        assert torch.equal(dgate.isnan(), at_up if act == "none" else at_gate | at_up)
+        assert torch.equal(dup.isnan(), at_gate)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [2, 130])
 def test_in_a_graph(m):
     n, k = 260, 700
