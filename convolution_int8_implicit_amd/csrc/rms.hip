@@ -101,11 +101,11 @@ __global__ __launch_bounds__(threads_of(TPR)) void rms_kernel(RmsArgs a)
     };
     const float ss = row_sum<TPR>(squares(1.0f), red[0]);
     float rstd = 1.0f / sqrtf(ss / (float)a.c + a.eps);
-    // Squares of values past 2^63 overflow: the same in units of 2^80, beside which eps is nothing.
+    // Squares of values past 2^63 overflow: the same in units of 2^80 (where an eps of ordinary size is nothing).
     const bool over = ss > 3.4e38f;
     if (TPR > 64 ? over : __any(over)) {
         const float big = row_sum<TPR>(squares(0x1p-80f), red[1]);
-        if (over) rstd = 0x1p-80f / sqrtf(big / (float)a.c);
+        if (over) rstd = 0x1p-80f / sqrtf(big / (float)a.c + a.eps * 0x1p-80f * 0x1p-80f);
     }
     if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll

@@ -320,6 +320,19 @@ def test_extreme_rows(c):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("c", [100, 1000, 3000, 20000])
+def test_rows_past_the_largest_square_with_a_large_eps(c):
+    """eps counts also in a row whose squares overflow."""
+    x = torch.zeros(3, c)
+    x[:, c // 3] = torch.tensor([2e19, -3e20, 1e10])
+    for eps in (1e34, 3e36, 3e38):
+        note(f"rows of {c}, eps {eps}")
+        y, _, rstd = ifx.rms_norm(x.cuda(), eps=eps)
+        eps32 = float(np.float32(eps))
+        check_rms(y, x, rstd, None, eps32, "f32")
+
+
+@pytest.mark.gpu
 def test_empty():
     w = torch.ones(40, device="cuda")
     none = torch.empty(0, 40, device="cuda", dtype=torch.bfloat16)
