@@ -186,7 +186,7 @@ class NormPointwise4:
 class FeedForwardState(NamedTuple):
     """What GatedFeedForward8.forward keeps for its gradient."""
     q: Fp8            # the normalised rows in 8 bits
-    h: torch.Tensor   # the sum of input and residual
+    h: torch.Tensor   # the sum of input and residual (without one the input itself where the layer does not train)
     rstd: torch.Tensor
     hidden: Fp8       # the gated pair's result in 8 bits
 
@@ -207,8 +207,9 @@ class GatedFeedForward8:
 
     w_gate and w_up float [hidden, c], w_down float [c, hidden], rounded once, with `train` their transposes too;
     norm_weight float32 [c].  forward() serves and trains, backward() gives the gradients of what forward() kept: its
-    products round a gradient to `grad_format` with a power of two per block of 128.  A result of a call with a stream is
-    memory of that stream.
+    products round a gradient to `grad_format` with a power of two per block of 128.  With `train` nothing that forward()
+    keeps is the caller's: its input may change before backward().  A result of a call with a stream is memory of that
+    stream.
     """
 
     def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
@@ -220,7 +221,9 @@ class GatedFeedForward8:
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None):
         """(y, what backward() needs): y of x's shape and type, x [..., c]."""
-        q, h, rstd = rms_norm_fp8(x, self.norm_weight, residual, self.eps, stream=stream)
+        own = residual is None and self.turned is not None  # a sum of its own, though it is x's values
+        q, h, rstd = rms_norm_fp8(x, self.norm_weight, residual, self.eps,
+                                  sum_out=_alloc(x, stream, x.dtype, *x.shape) if own else None, stream=stream)
         hidden = gated_fp8(q, self.gate, self.up, self.act, stream=stream)
         y = fp8_matmul(hidden, self.down, None, h.view(q.rows, q.k), ACT_NONE, x.dtype, stream=stream)
         return y.view(x.shape), FeedForwardState(q, h, rstd, hidden)

@@ -179,3 +179,18 @@ def test_hidden_values_past_float16():
     grads = ff.backward(full(tokens, c, v=2.0 ** -10), st)
     assert torch.equal(grads.down, torch.full((c, hidden), tokens * 2.0 ** 8, device="cuda"))
     assert all(bool(torch.isfinite(g).all()) for g in grads)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [5, 70])
+def test_input_that_changes_before_the_gradient(tokens):
+    """What forward() keeps for the gradient is not the input's memory, with a residual and without one."""
+    note(f"layer of {tokens} tokens, input overwritten")
+    ff, _ = layer(256, 640)
+    for residual in (False, True):
+        x, r, dy = (torch.randn(tokens, 256, device="cuda").to(torch.bfloat16) for _ in range(3))
+        expect = ff.backward(dy, ff.forward(x, r if residual else None)[1])
+        _, st = ff.forward(x, r if residual else None)
+        x.mul_(2.0)
+        r.zero_()
+        assert all(torch.equal(a, b) for a, b in zip(ff.backward(dy, st), expect))
