@@ -235,6 +235,8 @@ class GatedFeedForward8:
         q, h, rstd, hidden = state
         gate_t, up_t, down_t = self.turned
         fmt, dtype = self.grad_format, h.dtype
+        if dy.shape[-1:] != (q.k,) or dy.numel() != h.numel() or dy.dtype != dtype:
+            raise ValueError(f"dy of shape {tuple(h.shape)} and {dtype} expected")
         dy2 = dy.view(q.rows, q.k)
 
         def weight_grad(grad, values):

@@ -21,6 +21,17 @@ def values(q):
     return lowp.fp8_values(q.codes.cpu().numpy(), q.scales.cpu().numpy(), q.k, q.format)
 
 
+def test_gradients_of_another_shape_are_refused():
+    """Also where the sizes' product is right: its values would be taken for other columns'."""
+    ff = model.GatedFeedForward8.__new__(model.GatedFeedForward8)
+    ff.turned, ff.grad_format = (None,) * 3, ifx.FP8_E5M2
+    h = torch.empty(2, 3, 32, device="meta", dtype=torch.bfloat16)
+    st = model.FeedForwardState(ifx.fp8_empty(6, 32, device="meta"), h, None, None)
+    for bad in (h.view(32, 6), h.view(6, 2, 16), h[:1], h.float(), h.view(-1)):
+        with pytest.raises(ValueError, match="shape"):
+            ff.backward(bad, st)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("tokens,c,hidden,kind", [(1, 256, 640, "bf16"), (7, 100, 333, "f16"), (40, 257, 500, "bf16"),
                                                   (130, 384, 1000, "f32"), (600, 512, 1290, "bf16")])
