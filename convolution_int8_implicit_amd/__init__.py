@@ -707,6 +707,17 @@ def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
     return _pitch(t)[2]
 
 
+def _shares(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors of one shape and type, rows at a pitch each (_pitch), have an element in common."""
+    rows, c, ld = _pitch(a)
+    ld_b = _pitch(b)[2]
+    d = (b.data_ptr() - a.data_ptr()) // a.element_size()
+    if rows == 0 or d >= (rows - 1) * ld + c or -d >= (rows - 1) * ld_b + c:
+        return False
+    # side by side in the rows of a wider tensor, or not
+    return ld != ld_b or d % ld < c or ld - d % ld < c
+
+
 def group_norm_kernel_name(d: GnDesc, form: int = 0) -> str:
     """The (first) kernel instance that ifx_group_norm (form 0), its gradient (1) or its 4-bit form (2) launches
     for d, as profilers print it (host-only query)."""
@@ -969,8 +980,8 @@ def gated_fp8(x: Fp8, w_gate: Fp8, w_up: Fp8, act: int = ACT_SILU, out: Optional
 
 def gated_backward(dy: torch.Tensor, x: Fp8, w_gate: Fp8, w_up: Fp8, act: int = ACT_SILU, out=None, stream=None):
     """Gradient of gated at its two projections, which are computed anew (ifx_gated_backward) ->
-    (dgate, dup) of dy's type and shape; out: a pair of such tensors.  The gradients of x and of the weights are
-    products of these (fp8_quantize, fp8_quantize_t, fp8_matmul)."""
+    (dgate, dup) of dy's type and shape; out: a pair of such tensors, one of which may be dy.  The gradients of x and of
+    the weights are products of these (fp8_quantize, fp8_quantize_t, fp8_matmul)."""
     index = _on_device(dy, *x[:2], *w_gate[:2], *w_up[:2], *(out if out is not None else ()))
     d = _gated_desc(x, w_gate, w_up, act, dy.dtype)
     if dy.shape != (d.m, d.n):
@@ -980,6 +991,8 @@ def gated_backward(dy: torch.Tensor, x: Fp8, w_gate: Fp8, w_up: Fp8, act: int = 
         out = (_alloc(dy, stream, dy.dtype, d.m, d.n), _alloc(dy, stream, dy.dtype, d.m, d.n))
     else:
         d.ld_y, d.ld_up = _like(out[0], dy, "out[0]"), _like(out[1], dy, "out[1]")
+        if _shares(*out):
+            raise ValueError("out: the two gradients share memory")
     _check(lib().ifx_gated_backward(d, dy.data_ptr(), *_gated_addrs(x, w_gate, w_up), out[0].data_ptr(), out[1].data_ptr(),
                                     _raw_stream(stream, index)), "ifx_gated_backward")
     return out
@@ -989,17 +1002,6 @@ def _rms_desc(x: torch.Tensor, eps: float) -> RmsDesc:
     rows, c, ld = _pitch(x)
     _fits(rows, c)
     return RmsDesc(rows, c, _type(x.dtype), eps, ld, c, c, c, c, c)
-
-
-def _shares(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether two tensors of one shape and type, rows at a pitch each (_pitch), have an element in common."""
-    rows, c, ld = _pitch(a)
-    ld_b = _pitch(b)[2]
-    d = (b.data_ptr() - a.data_ptr()) // a.element_size()
-    if rows == 0 or d >= (rows - 1) * ld + c or -d >= (rows - 1) * ld_b + c:
-        return False
-    # side by side in the rows of a wider tensor, or not
-    return ld != ld_b or d % ld < c or ld - d % ld < c
 
 
 def _rms_forward(x, weight, residual, eps, sum_out, stream, out=None):

@@ -92,6 +92,23 @@ def test_binding_refusals_need_no_device(monkeypatch):
         ifx.gated(*good, dtype=torch.int8)
 
 
+def test_gradients_in_one_memory_are_refused(monkeypatch):
+    monkeypatch.setattr(ifx, "_on_device", lambda *ts: 0)
+    monkeypatch.setattr(ifx, "_raw_stream", lambda stream, index: 0)
+
+    class Lib:
+        def ifx_gated_backward(self, *args):
+            return 0
+    monkeypatch.setattr(ifx, "lib", Lib)
+    q = [ifx.fp8_empty(rows, 32, device="meta") for rows in (4, 6, 6)]
+    dy, other, wide = torch.zeros(4, 6), torch.zeros(4, 6), torch.zeros(4, 20)
+    for out in ((dy, other), (other, dy), (wide[:, :6], wide[:, 6:12]), (wide[:, 14:], wide[:, :6])):
+        assert ifx.gated_backward(dy, *q, out=out) is out
+    for out in ((dy, dy), (other, other), (wide[:, :6], wide[:, 5:11]), (wide[:, 9:15], wide[:, 4:10])):
+        with pytest.raises(ValueError, match="share"):
+            ifx.gated_backward(dy, *q, out=out)
+
+
 # ------------------------------------------------------------------------------------------ GPU
 
 def gated_case(m, n, k, seed):
