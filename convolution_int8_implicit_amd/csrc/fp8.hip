@@ -397,9 +397,10 @@ hipError_t launch_fp8(Fp8Args a, Fp8Mode mode, hipStream_t s)
     if (mode == kProduct) return a.a_format ? rows_of_type<kProduct, 1>(a, s) : rows_of_type<kProduct, 0>(a, s);
     if (mode == kGatedGrad) return rows_of_type<kGatedGrad, 0>(a, s);
     if (!a.codes) return rows_of_type<kGated, 0>(a, s);
-    // A block's 128 columns are eight workgroups': their values in 32 bits first, then the rounding in a launch of its own
-    // (4 us).  One launch whose workgroups take 128 columns of both weights reads no faster than 35 GB/s a CU: 1 x 8192 x
-    // 2048 18.2 us against 12.1, 1 x 2048 x 8192 59.6 against 12.1 (1 x 1000 x 500 9.4 against 11.7).
+    // A block's 128 columns are eight workgroups': their values in 32 bits first, by the kernel of float32 results, then the
+    // rounding in a launch of its own (4 us).  One launch whose workgroups take 128 columns of both weights reads no faster
+    // than 35 GB/s a CU: 1 x 8192 x 2048 18.2 us against 12.1, 1 x 2048 x 8192 59.6 against 12.1 (1 x 1000 x 500 9.4 against
+    // 11.7).
     a.y = a.ws;
     a.type = 0;
     a.ld_y = a.n;

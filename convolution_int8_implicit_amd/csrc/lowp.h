@@ -345,7 +345,8 @@ __device__ __forceinline__ uint2 fp8_codes(const float (&f)[8], unsigned s)
 typedef __bf16 lowp_v8b __attribute__((ext_vector_type(8)));
 
 // 32 codes times their block's power of two, in four vectors of bfloat16.  Exact from scale byte 10 on (e4m3; 17 for
-// e5m2), below which the smallest codes pass the smallest normal bfloat16.
+// e5m2), below which the smallest codes pass the smallest normal bfloat16, to 246 (239), above which codes of 2^128 and
+// more, which float32 does not hold either, become infinities.
 template <int FMT>
 __device__ __forceinline__ void fp8_widen(ifx_v4i lo, ifx_v4i hi, unsigned s, lowp_v8b (&out)[4])
 {

@@ -629,13 +629,14 @@ ifx_status ifx_fp8_dequantize(const uint8_t *codes, const uint8_t *scales, int32
  * (e4m3), both of k columns:
  *   y[i, j] = act(sum_c A[i, c] W[j, c] + bias[j] + residual[i, j])
  * accumulated in 32-bit floating point and rounded once to `type`.  Results of
- * 16 bits (and 8, below) are computed on the 8-bit matrix units, which cut each
- * of the eight products that they add at a time off below 2^-13 of the largest:
- * 1.5e-5 of a result on normally distributed values, at most 7 2^-13 of the sum
- * of its terms' magnitudes.  IFX_F32 results are computed on the 16-bit ones, in
- * full precision at half the rate; there, codes whose value lies below the
- * smallest normal bfloat16 (possible where s < 10, in e5m2 s < 17) may count as
- * zero.  The sum of one (m, n, k) and type is taken in one order, so results
+ * 16 bits are computed on the 8-bit matrix units, which cut each of the eight
+ * products that they add at a time off below 2^-13 of the largest: 1.5e-5 of a
+ * result on normally distributed values, at most 7 2^-13 of the sum of its
+ * terms' magnitudes.  IFX_F32 results are computed on the 16-bit ones, in full
+ * precision at half the rate; there, codes whose value lies below the smallest
+ * normal bfloat16 (possible where s < 10, in e5m2 s < 17) may count as zero, and
+ * codes whose value is 2^128 or more, past float32 (s >= 247, in e5m2 s >= 240:
+ * a block with a value next to the largest float32), count as infinities.  The sum of one (m, n, k) and type is taken in one order, so results
  * are the same from call to call.  A NaN block makes its row of y (A) or its
  * column (W) NaN.
  *   bias      DEVICE float32 [n], 4-byte aligned, or NULL
@@ -664,7 +665,10 @@ ifx_status ifx_fp8_matmul(const ifx_fp8_desc *d, const uint8_t *a_codes, const u
  *   gate = X G^T, up = X U^T, y = act(gate) * up
  * Sums are taken as ifx_fp8_matmul's and held in 32 bits as y is; ifx_gated rounds y once
  * to `type`, ifx_gated_fp8 to e4m3 codes of m rows and n columns (the operand
- * of the projection back).  ifx_gated_backward takes the gradient dy of y,
+ * of the projection back).  Codes come of sums on the 8-bit matrix units, but of
+ * up to 16 rows (where ifx_gated_workspace_bytes is not 0) of sums taken as
+ * IFX_F32 results' are, so a row's codes may differ by a rounding between a batch of
+ * up to 16 rows and a larger one.  ifx_gated_backward takes the gradient dy of y,
  * recomputes both projections and writes
  *   dgate = dy * up * act'(gate) (for ReLU 0 where gate <= 0),  dup = dy * act(gate)
  * to `type`, from which the products with G, U and X give the gradients of X,
@@ -714,12 +718,12 @@ ifx_status ifx_gated_backward(const ifx_gated_desc *d, const void *dy, const uin
  *           ld_x (x; the gradient's h), ld_res, ld_h, ld_y (y, dx), ld_dy and
  *           ld_dh >= c; an absent operand's is not looked at.  h may be x or
  *           the residual, y may be x, the residual or neither, not h; dx may be
- *           dy, h or dh (same pitches)
+ *           dy, h or dh (same pitches each time)
  *   weight  DEVICE float32 [c], 4-byte aligned, or NULL (1)
  *   dweight, rstd  DEVICE float32 [c] and [rows], 4-byte aligned
  *   rows    >= 0 (0: only dweight is written, zeros); 1 <= c <= 24576; eps >= 0.
- *           Squares are summed in 32 bits: with eps = 0 a row's root mean square
- *           has to be at least 2^-60
+ *           Squares are summed in 32 bits: with eps below 2^-120 a row's root
+ *           mean square has to be at least 2^-60
  *   ws      DEVICE, 16-byte aligned, at least ifx_rms_norm_workspace_bytes (may
  *           be NULL where that is 0 or dweight is NULL)
  * Errors (nothing is launched): IFX_E_NULL, IFX_E_SHAPE (also more rows than a

@@ -593,3 +593,30 @@ def test_offsets_past_32_bits():
     few = (t.codes.cpu().numpy(), t.scales.cpu().numpy())
     check_product(y[-40:], 40, 24, k, few, (w.codes.cpu().numpy(), w.scales.cpu().numpy()), None, None, 0, "bf16")
     assert not y[:-40].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 6, 40, 300])
+@pytest.mark.parametrize("fmt,byte", [(0, 247), (1, 240)])
+def test_matmul_largest_scales(m, fmt, byte):
+    """The largest scales that a rounding gives.  Codes whose value float32 holds multiply exactly; one of 2^128 is finite
+    in a 16-bit result, whose matrix instruction adds exponents, and infinite in float32, whose operands are widened."""
+    n, k = 70, 700
+    note(f"scale {byte} of format {fmt}, {m} rows")
+    a, w, _, _ = product_case(m, n, k, 31 + m, fmt)
+    a[1][a[1] > 0] = byte
+    w[1][w[1] > 0] = 16
+    a[0][(a[0] & 127) >= 0x78] &= 0x83  # from 256 (32768) on
+    for kind in ("f32", "bf16"):
+        check_product(ifx.fp8_matmul(tensor_of(a, k, fmt), tensor_of(w, k), dtype=TYPES[kind]), m, n, k, a, w, None, None, 0,
+                      kind, fmt)
+    a[0][1, m - 1, 3] = 0x78  # 256 2^120 or 32768 2^113
+    w[0][1, 3, 3], w[0][1, 4, 3], w[0][1, 5, 3] = 0x38, 0xb8, 0
+    A, W = tensor_of(a, k, fmt), tensor_of(w, k)
+    check_product(ifx.fp8_matmul(A, W, dtype=torch.bfloat16), m, n, k, a, w, None, None, 0, "bf16", fmt)
+    y = f64(ifx.fp8_matmul(A, W, dtype=torch.float32))
+    assert y[m - 1, 3] == np.inf and y[m - 1, 4] == -np.inf and np.isnan(y[m - 1, 5])
+    assert np.isfinite(y[:m - 1]).all()
+    # such a value comes of a rounding: of the largest float32
+    q = ifx.fp8_quantize(torch.full((1, 1), torch.finfo(torch.float32).max, device="cuda"), fmt)
+    assert int(q.scales[0, 0, 0]) == byte and int(q.codes[0, 0, 0]) == 0x78 and bool(ifx.fp8_dequantize(q, torch.float32).isinf())

@@ -362,3 +362,17 @@ def test_empty_and_refusals():
     with pytest.raises(ifx.IfxError):
         ifx.gated(w, w, w, act=9)
     assert ifx.gated_fp8(w, x, x).codes.shape == (0, 6, 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,k", [(300, 700), (1000, 5000)])
+def test_codes_of_a_row_alone_and_in_a_batch(n, k):
+    """Rows of a batch of 17, and each alone, among three and among 16 of them, where other kernels run: sums differ by
+    their bounds only."""
+    note(f"gated to codes, {n} x {k}")
+    q, _ = gated_case(17, n, k, 41)
+    X, G, U = (tensor_of(t, k) for t in q)
+    y, _, _, tol, _, _ = bounds(q, k, 2, "bf16")
+    for rows in [slice(0, 17), slice(0, 16), slice(2, 5)] + [slice(i, i + 1) for i in (0, 7, 16)]:
+        part = ifx.Fp8(X.codes[:, rows].contiguous(), X.scales[:, rows].contiguous(), k)
+        check_fp8(ifx.gated_fp8(part, G, U), y[rows], tol[rows], n)
