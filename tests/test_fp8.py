@@ -595,6 +595,67 @@ def test_offsets_past_32_bits():
     assert not y[:-40].any()
 
 
+def whole_excess(got, exact, tol, kind):
+    """excess() of whole large results, on the GPU."""
+    low, high = ((exact + sign * tol).to(TYPES[kind]).double() for sign in (-1, 1))
+    out = torch.maximum(low - got.double(), got.double() - high).clamp_(min=0)
+    return float(out.max()) if not bool(out.isnan().any()) else np.inf
+
+
+def cuda64(q, k, fmt=0):
+    return torch.from_numpy(np.ascontiguousarray(lowp.fp8_values(q[0], q[1], k, fmt))).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,fmt", [("bf16", 0), ("bf16", 1), ("f16", 0), ("f16", 1), ("f32", 0), ("f32", 1)])
+@pytest.mark.parametrize("extra", [0, 64, 3])
+def test_matmul_many_large_tiles(kind, fmt, extra):
+    """Large tiles of either format of A and every type: the ring refilled many times, three words of scales, whole tiles
+    and edges inside a tile, results past the caches' size in rows that fill 128-byte lines (extra 0 and 64) and rows
+    that share them; bias and residual in turn.  Every result is checked, and what lies beside the rows."""
+    m, n, k = 4200, 4160, 1200
+    note(f"large tiles {m} x {n} x {k} {kind} format {fmt}, rows of {n + extra}")
+    rng = np.random.default_rng(21 + fmt)
+    a, w = random_codes(rng, m, k, fmt, 112 if fmt else 118, 118 if fmt else 124), random_codes(rng, n, k, 0, 118, 124)
+    if kind == "f16":  # keeps float16 results finite
+        a = (a[0], a[1] - 6 * (a[1] > 0).astype(np.uint8))
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    bias = torch.randn(n, generator=gen, device="cuda") * 30
+    res = (torch.randn(m, n, generator=gen, device="cuda") * 30).to(TYPES[kind])
+    av, wv = cuda64(a, k, fmt), cuda64(w, k)
+    z, size = av @ wv.t(), av.abs() @ wv.abs().t()
+    A, W = tensor_of(a, k, fmt), tensor_of(w, k)
+    for b, r in ((bias, None), (None, res)):
+        wide = torch.full((m, n + extra), 3.0, dtype=TYPES[kind], device="cuda")
+        ifx.fp8_matmul(A, W, b, r, ifx.ACT_NONE, out=wide[:, :n])
+        term = (b if r is None else r).double()
+        assert whole_excess(wide[:, :n], z + term, sum_bound(k, kind) * (size + term.abs()), kind) == 0
+        assert bool((wide[:, n:] == 3).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n", [(6, 40), (70, 40), (300, 520), (4100, 4100)])
+def test_infinities_of_e5m2_in_every_kernel(m, n, kind):
+    """An infinity of e5m2 gives infinities of its sign and W's, or NaN against a zero or a NaN, in its row alone."""
+    note(f"an infinity in {m} x {n} {kind}")
+    k = 200
+    rng = np.random.default_rng(m + n)
+    a, w = integer_codes(rng, m, k, 1), integer_codes(rng, n, k)
+    for row, code in ((3, 0x7c), (m - 1, 0xfc)):
+        a[0][1, row, 7] = code
+    w[0][1, :, 7] = 0x38  # 1
+    w[0][1, 5, 7], w[0][1, 6, 7], w[0][1, n - 1, 7] = 0, 0xb8, 0xb8
+    y = f64(ifx.fp8_matmul(tensor_of(a, k, 1), tensor_of(w, k), dtype=TYPES[kind]))
+    expect = np.full(n, np.inf)
+    expect[5], expect[6], expect[n - 1] = np.nan, -np.inf, -np.inf
+    assert np.array_equal(y[3], expect, equal_nan=True) and np.array_equal(y[m - 1], -expect, equal_nan=True)
+    rest = np.delete(np.arange(m), [3, m - 1])
+    av = torch.from_numpy(lowp.fp8_values(a[0][:, rest], a[1][:, rest], k, 1))
+    exact = av @ torch.from_numpy(lowp.fp8_values(*w, k)).t()
+    assert np.array_equal(y[rest], f64(exact.to(TYPES[kind])))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 6, 40, 300])
 @pytest.mark.parametrize("fmt,byte", [(0, 247), (1, 240)])

@@ -14,7 +14,7 @@ import torch
 
 import convolution_int8_implicit_amd as ifx
 from oracle import lowp
-from test_fp8 import integer_codes, random_codes, same_codes, sum_bound, tensor_of
+from test_fp8 import cuda64, integer_codes, random_codes, same_codes, sum_bound, tensor_of, whole_excess
 from test_mx4 import TYPES, excess, f64, note
 
 ACTS = {"none": 0, "relu": 1, "silu": 2}
@@ -362,6 +362,44 @@ def test_empty_and_refusals():
     with pytest.raises(ifx.IfxError):
         ifx.gated(w, w, w, act=9)
     assert ifx.gated_fp8(w, x, x).codes.shape == (0, 6, 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,act", [("bf16", "silu"), ("f16", "none"), ("f16", "silu"), ("f32", "silu")])
+@pytest.mark.parametrize("extra", [0, 64, 3])
+def test_many_large_tiles(kind, act, extra):
+    """Large tiles whose ring is refilled many times for both weights, three words of scales, whole tiles and edges inside
+    one, results past the caches' size in rows that fill 128-byte lines (extra 0 and 64) and rows that share them.  Every
+    result is checked, and what lies beside the rows."""
+    m, n, k = 4200, 2112, 1200
+    note(f"gated, large tiles {m} x {n} x {k} {kind} {act}, rows of {n + extra}")
+    q, _ = gated_case(m, n, k, 31)
+    X, G, U = (tensor_of(t, k) for t in q)
+    x, gv, uv = (cuda64(t, k) for t in q)
+    b = sum_bound(k, kind)
+    g, u, tg, tu = x @ gv.t(), x @ uv.t(), b * (x.abs() @ gv.abs().t()), b * (x.abs() @ uv.abs().t())
+    s = torch.sigmoid(g)
+    a, slope = (g * s, s + g * s * (1 - s)) if act == "silu" else (g, torch.ones_like(g))
+    more = (g.abs() + 4) * 2.0 ** -22 if act == "silu" else torch.zeros_like(g)
+    y = a * u
+    tol = a.abs() * tu + 1.1 * tg * (u.abs() + tu) + (2.0 ** -23 + more) * y.abs()
+
+    def results():
+        return torch.full((m, n + extra), 3.0, dtype=TYPES[kind], device="cuda")
+    out = results()
+    ifx.gated(X, G, U, ACTS[act], out=out[:, :n])
+    assert float(y.abs().max()) < 30000 and whole_excess(out[:, :n], y, tol, kind) == 0 and bool((out[:, n:] == 3).all())
+    if extra == 0 and kind == "bf16":
+        check_fp8(ifx.gated_fp8(X, G, U, ACTS[act]), f64(y), f64(tol), n)
+    d = torch.randn(m, n, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(TYPES[kind])
+    dg, du = results(), results()
+    ifx.gated_backward(d, X, G, U, ACTS[act], out=(dg[:, :n], du[:, :n]))
+    d = d.double()
+    tol_g = d.abs() * (1.1 * tu + 0.5 * tg * (u.abs() + tu) + (1.1 * more + 2.0 ** -22) * (u.abs() + tu))
+    tol_u = d.abs() * (1.1 * tg + (more + 2.0 ** -22) * a.abs())
+    assert whole_excess(dg[:, :n], d * u * slope, tol_g, kind) == 0
+    assert whole_excess(du[:, :n], d * a, tol_u, kind) == 0
+    assert bool((dg[:, n:] == 3).all()) and bool((du[:, n:] == 3).all())
 
 
 @pytest.mark.gpu
