@@ -161,7 +161,8 @@ __global__ __launch_bounds__(256) void fp8_quantize_t_kernel(const void *x, long
     }
 }
 
-// The values back: eight columns per thread, 8 bytes of codes in, one 16-byte store of a 16-bit type out.
+// The values back: eight columns per thread, 8 bytes of codes in, one 16-byte store of a 16-bit type out.  HBM-bound:
+// 8192 x 8192 to bf16 36.2 us, 5.6 TB/s, to float32 78, 4.3.
 template <int TYPE, int FMT>
 __global__ __launch_bounds__(256) void fp8_dequantize_kernel(const uint8_t *codes, const uint8_t *scales, int rows, int k,
                                                              int k1, int groups, void *y, long long ld, int past)
@@ -213,9 +214,10 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(const uint8_t *code
 //
 // For up to 16 rows of A.  A workgroup of kRowWaves waves takes 16 weight rows (of both weights in the gated forms); its
 // waves take panels in turn straight from memory, several requested at once, and the partial sums meet in LDS, added in
-// wave order.  What bounds it: the weights, read once (one row of 8192 x 8192, launch included, 12.8 us, 5.2 TB/s; 16 rows
-// 19.5).  From 17 rows on the tiles are as fast or faster: 32 rows of 8192 x 8192 20.0 us against 29.6 with two groups of
-// 16 rows here, 64 rows 22.1 against 45.8 (20 rows of 2048 x 8192 16.1 against 12.8 is the one loss seen).
+// wave order.  What bounds it: the weights, read once (one row of 8192 x 8192, launch included, 12.8 us, 5.2 TB/s, with
+// three weights in turn, which the memory-side cache holds in part, 16.6 with eight; 16 rows 19.5 and 20.5).  From 17 rows
+// on the tiles are as fast or faster: 32 rows of 8192 x 8192 20.0 us against 29.6 with two groups of 16 rows here, 64 rows
+// 22.1 against 45.8 (20 rows of 2048 x 8192 16.1 against 12.8 is the one loss seen).
 // The 16x16x128 instruction takes row l % 16 and 32 of the panel's columns from lane l; which 32 is the same on
 // both sides, so a lane takes the chunks that make its two loads whole 64-byte runs.  Lane l's results are column
 // l % 16 (a row of A here) and rows 4 (l / 16) .. + 3 (weight rows).

@@ -207,7 +207,8 @@ class GatedFeedForward8:
 
     w_gate and w_up float [hidden, c], w_down float [c, hidden], rounded once, with `train` their transposes too;
     norm_weight float32 [c].  forward() serves and trains, backward() gives the gradients of what forward() kept: its
-    products round a gradient to `grad_format` with a power of two per block of 128.  With `train` nothing that forward()
+    products round a gradient to `grad_format` with a power of two per block of 128, and the weights' gradients round n and
+    the gated pair's result, 8-bit already, once more in blocks of 128 tokens.  With `train` nothing that forward()
     keeps is the caller's: its input may change before backward().  A result of a call with a stream is memory of that
     stream.
     """
@@ -244,6 +245,7 @@ class GatedFeedForward8:
         # through the projection back, the gated pair, the two projections, the norm
         dhidden = fp8_matmul(fp8_quantize(dy2, fmt, stream=stream), down_t, dtype=dtype, stream=stream)
         dgate, dup = gated_backward(dhidden, q, self.gate, self.up, self.act, stream=stream)
+        # (dn's first half is kept in the layer's type, 2^-9 of it in bfloat16, where its operands carry 2^-3 and 2^-4)
         dn = fp8_matmul(fp8_quantize(dgate, fmt, stream=stream), gate_t, dtype=dtype, stream=stream)
         fp8_matmul(fp8_quantize(dup, fmt, stream=stream), up_t, None, dn, ACT_NONE, dtype, out=dn, stream=stream)
         dx, dnorm = rms_norm_backward(dn.view(h.shape), h, rstd, self.norm_weight, dy.view(h.shape), stream=stream)
