@@ -707,15 +707,13 @@ def _like(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
     return _pitch(t)[2]
 
 
-def _shares(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether two tensors of one shape and type, rows at a pitch each (_pitch), have an element in common."""
-    rows, c, ld = _pitch(a)
-    ld_b = _pitch(b)[2]
+def _shares(a: torch.Tensor, b: torch.Tensor, rows: int, c: int, ld_a: int, ld_b: int) -> bool:
+    """Whether two tensors of one type, each of `rows` rows of c elements at its pitch, have an element in common."""
     d = (b.data_ptr() - a.data_ptr()) // a.element_size()
-    if rows == 0 or d >= (rows - 1) * ld + c or -d >= (rows - 1) * ld_b + c:
+    if rows == 0 or d >= (rows - 1) * ld_a + c or -d >= (rows - 1) * ld_b + c:
         return False
     # side by side in the rows of a wider tensor, or not
-    return ld != ld_b or d % ld < c or ld - d % ld < c
+    return ld_a != ld_b or d % ld_a < c or ld_a - d % ld_a < c
 
 
 def group_norm_kernel_name(d: GnDesc, form: int = 0) -> str:
@@ -991,7 +989,7 @@ def gated_backward(dy: torch.Tensor, x: Fp8, w_gate: Fp8, w_up: Fp8, act: int = 
         out = (_alloc(dy, stream, dy.dtype, d.m, d.n), _alloc(dy, stream, dy.dtype, d.m, d.n))
     else:
         d.ld_y, d.ld_up = _like(out[0], dy, "out[0]"), _like(out[1], dy, "out[1]")
-        if _shares(*out):
+        if _shares(*out, d.m, d.n, d.ld_y, d.ld_up):
             raise ValueError("out: the two gradients share memory")
     _check(lib().ifx_gated_backward(d, dy.data_ptr(), *_gated_addrs(x, w_gate, w_up), out[0].data_ptr(), out[1].data_ptr(),
                                     _raw_stream(stream, index)), "ifx_gated_backward")
@@ -1015,10 +1013,10 @@ def _rms_forward(x, weight, residual, eps, sum_out, stream, out=None):
         d.ld_y = _like(out, x, "out")
     if sum_out is not None:
         d.ld_h = _like(sum_out, x, "sum_out")
-        if out is not None and _shares(out, sum_out):
+        if out is not None and _shares(out, sum_out, d.rows, d.c, d.ld_y, d.ld_h):
             raise ValueError("out and sum_out share memory")
         return d, sum_out, True
-    if residual is None and (out is None or not _shares(out, x)):
+    if residual is None and (out is None or not _shares(out, x, d.rows, d.c, d.ld_y, d.ld_x)):
         return d, x, False
     return d, _alloc(x, stream, x.dtype, *x.shape), True
 
