@@ -14,7 +14,8 @@ import torch
 
 import convolution_int8_implicit_amd as ifx
 from oracle import lowp
-from test_fp8 import cuda64, integer_codes, random_codes, same_codes, sum_bound, tensor_of, whole_excess
+from test_fp8 import integer_codes, random_codes, same_codes, sum_bound, tensor_of
+from test_fp8 import cuda64, whole_excess
 from test_mx4 import TYPES, excess, f64, note
 
 ACTS = {"none": 0, "relu": 1, "silu": 2}
